@@ -328,6 +328,60 @@ W8A8_API w8a8_status w8a8_linear_gelu(const void* h, const int8_t* wq, const flo
                                       int64_t M, int64_t N, int64_t K, w8a8_stream_t stream);
 
 /*
+ * Norms of queries and keys with the position rotation, in one pass over the
+ * output of a block's QKV linear layer (the step between that layer and the
+ * attention).  For every token m and head, over its D = head_dim values x:
+ *   n[i] = x[i] * rsqrt(sum_j x[j]^2 / D + eps) * weight[i]
+ * and the first R = rot_dim values turn in pairs by row r of a table of
+ * angles (r = positions[m], or m where positions is NULL):
+ *   y[a] = n[a] * cos[r,t] - n[b] * sin[r,t]
+ *   y[b] = n[b] * cos[r,t] + n[a] * sin[r,t]        t = 0 .. R/2 - 1
+ * with (a, b) = (t, t + R/2) for W8A8_ROPE_HALVES and (2t, 2t + 1) for
+ * W8A8_ROPE_PAIRS; the other D - R values keep n.  All in binary32, rounded
+ * once to bf16.
+ *
+ *   q, k        bf16 [M, heads, head_dim], the last dimension contiguous, ld*
+ *               the stride of a token and hs* of a head, in elements (multiples
+ *               of 8, 0 allowed for inputs): views into one QKV buffer, or
+ *               head-major tensors.  heads_q or heads_k may be 0 (its pointers
+ *               are then not used).
+ *   q_out,k_out the same shapes with their own strides; the heads of an output
+ *               may not overlap one another.  An output may be its own input
+ *               (same pointer and strides: in place); any other overlap of an
+ *               output with another array is undefined.
+ *   q_weight, k_weight  bf16 [head_dim], or NULL for ones
+ *   cos, sin    fp32 [table_rows, rot_dim/2], both or neither (norm only:
+ *               rot_dim, table_rows and layout's pairing are then not used)
+ *   positions   int32 [M] or NULL (then table_rows >= M).  A position outside
+ *               [0, table_rows) reads nothing: the token's rotated values
+ *               become NaN.
+ * head_dim a multiple of 8 in 16..256, rot_dim a multiple of 16 up to head_dim,
+ * heads up to 65536, eps >= 0 finite.  A row whose squares overflow binary32
+ * becomes 0 (finite values) as the formula in binary32 gives it.
+ */
+enum { W8A8_ROPE_HALVES = 0, W8A8_ROPE_PAIRS = 1 };
+
+typedef struct {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    const void* q_weight;
+    const void* k_weight;
+    const float* cos;
+    const float* sin;
+    const int32_t* positions;
+    int64_t M, table_rows;
+    int64_t ldq, hsq, ldk, hsk;
+    int64_t ldq_out, hsq_out, ldk_out, hsk_out;
+    int32_t heads_q, heads_k, head_dim, rot_dim;
+    int32_t layout;           /* W8A8_ROPE_HALVES or W8A8_ROPE_PAIRS */
+    float eps;
+} w8a8_qk_desc;
+
+W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t stream);
+
+/*
  * A chain of W8A8 linear layers as one CUDA graph (the paper drops its
  * kernel into every linear layer of the DiT, abstract; a DiT block runs
  * four: attention QKV, attention output, MLP up, MLP down).  Each layer is

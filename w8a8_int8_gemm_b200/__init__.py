@@ -31,6 +31,7 @@ __all__ = [
     "w8a8_quantize_act_fp8", "w8a8_quantize_weight_fp8", "w8a8_gemm_fp8", "w8a8_gemm_fp8_ex",
     "w8a8_gemm_fp8_f32", "w8a8_gemm_fp8_f32_ex", "w8a8_linear_fp8",
     "w8a8_quantize_act_gelu", "w8a8_gelu", "w8a8_linear_gelu", "ACT_NONE", "ACT_GELU",
+    "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS",
     "LinearDesc", "Chain", "linear_layer", "w8a8_chain_create", "w8a8_chain_launch", "w8a8_chain_layers",
     "w8a8_chain_destroy",
     "w8a8_select_config",
@@ -45,6 +46,8 @@ W8A8_OK = 0
 W8A8_ERR_TIMEOUT = 5
 ACT_NONE = 0   # W8A8_ACT_NONE
 ACT_GELU = 1   # W8A8_ACT_GELU
+ROPE_HALVES = 0  # W8A8_ROPE_HALVES
+ROPE_PAIRS = 1   # W8A8_ROPE_PAIRS
 
 
 class W8A8Error(RuntimeError):
@@ -68,6 +71,16 @@ class LinearDesc(ctypes.Structure):
                 ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ws_xq", ctypes.c_void_p),
                 ("ws_scale_a", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("input_act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QkDesc(ctypes.Structure):
+    """w8a8_qk_desc: the arguments of w8a8_qk_norm_rope."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "cos", "sin",
+                                                "positions")]
+                + [(n, ctypes.c_int64) for n in ("M", "table_rows", "ldq", "hsq", "ldk", "hsk", "ldq_out", "hsq_out",
+                                                 "ldk_out", "hsk_out")]
+                + [(n, ctypes.c_int32) for n in ("heads_q", "heads_k", "head_dim", "rot_dim", "layout")]
+                + [("eps", ctypes.c_float)])
 
 
 def _load() -> ctypes.CDLL:
@@ -100,6 +113,7 @@ def _load() -> ctypes.CDLL:
         "w8a8_quantize_act_gelu": ([p, i64, i64, i64, p, i64, p, p], ctypes.c_int),
         "w8a8_gelu": ([p, i64, i64, i64, p, i64, p], ctypes.c_int),
         "w8a8_linear_gelu": ([p, p, p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
+        "w8a8_qk_norm_rope": ([ctypes.POINTER(QkDesc), p], ctypes.c_int),
         "w8a8_chain_create": ([ctypes.POINTER(LinearDesc), i32, ctypes.POINTER(p)], ctypes.c_int),
         "w8a8_chain_launch": ([p, p], ctypes.c_int),
         "w8a8_chain_layers": ([p], i32),
@@ -541,6 +555,68 @@ def w8a8_linear_gelu(h, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a
                                  _ptr(l["ws_xq"]), _ptr(l["ws_scale_a"]), l["M"], l["N"], l["K"],
                                  _stream(stream, h.device)), "w8a8_linear_gelu")
     return l["out"]
+
+
+# ------------------------------------------------- between QKV and attention
+
+
+def _heads(t: torch.Tensor, name: str, dim: int | None = None) -> tuple:
+    """Checks a bf16 [tokens, heads, head_dim] tensor; its (token, head) strides in elements."""
+    _need(t, name, torch.bfloat16, 3)
+    rows, heads, d = t.shape
+    if dim is not None and d != dim:
+        raise ValueError(f"{name} must have head dimension {dim}, got {d}")
+    hs = t.stride(1) if heads > 1 else d
+    return (t.stride(0) if rows > 1 else max(1, heads) * hs), hs
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device the given tensors (None skipped) share."""
+    dev = [t.device for t in tensors if t is not None]
+    if any(d != dev[0] for d in dev):
+        raise ValueError(f"tensors are on different devices: {sorted({str(d) for d in dev})}")
+    return dev[0]
+
+
+def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
+                      layout: int = ROPE_HALVES, q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of q [M, Hq, D] and k [M, Hk, D] and the rotation of its first 2 * cos.shape[1]
+    values, in one pass -> (q_out, k_out), allocated here (contiguous) if not given; q_out=q, k_out=k works in
+    place.  q and k may be strided views, e.g. of one QKV buffer.  cos, sin fp32 [rows, R/2], read at row
+    positions[m] (int32 [M]) or m; without them the norm alone."""
+    ldq, hsq = _heads(q, "q")
+    M, hq, D = q.shape
+    ldk, hsk = _heads(k, "k", D)
+    if k.shape[0] != M:
+        raise ValueError(f"q has {M} tokens, k has {k.shape[0]}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need_contig(w, name, torch.bfloat16, (D,))
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    rows = rot = 0
+    if cos is not None:
+        _need(cos, "cos", torch.float32, 2)
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        _need_contig(cos, "cos", torch.float32, (rows, rot // 2))
+        _need_contig(sin, "sin", torch.float32, (rows, rot // 2))
+    if positions is not None:
+        _need_contig(positions, "positions", torch.int32, (M,))
+    if q_out is None:
+        q_out = torch.empty((M, hq, D), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(tuple(k.shape), dtype=torch.bfloat16, device=q.device)
+    ldqo, hsqo = _heads(q_out, "q_out", D)
+    ldko, hsko = _heads(k_out, "k_out", D)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("outputs must have the shapes of q and k")
+    dev = _one_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
+    desc = QkDesc(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                  _ptr(positions), M, rows, ldq, hsq, ldk, hsk, ldqo, hsqo, ldko, hsko, hq, k.shape[1], D, rot,
+                  int(layout), float(eps))
+    with torch.cuda.device(dev):
+        _check(_lib.w8a8_qk_norm_rope(ctypes.byref(desc), _stream(stream, dev)), "w8a8_qk_norm_rope")
+    return q_out, k_out
 
 
 # ------------------------------------------------- chains of linear layers

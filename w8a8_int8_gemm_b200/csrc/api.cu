@@ -54,8 +54,6 @@ w8a8_status current_device(DeviceInfo* out) {
   return d.supported ? W8A8_OK : W8A8_ERR_UNSUPPORTED_DEVICE;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 w8a8_status check_gemm_shape(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || M > kMaxMN || N > kMaxMN) return W8A8_ERR_INVALID_ARG;
   if (K < 16 || K > kMaxK || K % 16 != 0) return W8A8_ERR_INVALID_ARG;
@@ -119,12 +117,6 @@ w8a8_gemm_config select(int64_t M, int64_t N, int64_t K, int sms, bool allow_pai
   return cfg;
 }
 
-w8a8_status from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return W8A8_OK;
-  if (e == cudaErrorInvalidValue) return W8A8_ERR_INVALID_ARG;
-  return W8A8_ERR_LAUNCH;
-}
-
 w8a8_status gemm_common(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
                         const void* bias, void* out, int64_t M, int64_t N, int64_t K,
                         const w8a8_gemm_config* user_cfg, GemmOut kind, cudaStream_t stream,
@@ -158,7 +150,7 @@ w8a8_status gemm_common(const int8_t* xq, const int8_t* wq, const float* scale_a
   a.l2_bytes = dev.l2_bytes;
   a.overlap_prologue = overlap_prologue;
   GemmConfig c{cfg.block_m, cfg.block_n, cfg.stages, cfg.grid, cfg.raster_group};
-  return from_cuda(launch_gemm(a, c, stream));
+  return status_of(launch_gemm(a, c, stream));
 }
 
 w8a8_status quantize_common(bool act, const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* xq, int64_t ldxq,
@@ -185,7 +177,7 @@ w8a8_status quantize_common(bool act, const void* x, int64_t M, int64_t K, int64
     e = act ? launch_quantize_act(x, M, K, ldx, xq, ldxq, scale, stream)
             : launch_quantize_weight(w, M, K, ldx, xq, ldxq, scale, stream);
   }
-  return from_cuda(e);
+  return status_of(e);
 }
 
 }  // namespace
@@ -320,7 +312,7 @@ w8a8_status w8a8_linear_fused(const void* x, const int8_t* wq, const float* scal
   a.ldx = K;
   a.sync = ws_sync;
   GemmConfig c{cfg.block_m, cfg.block_n, cfg.stages, cfg.grid, cfg.raster_group};
-  return from_cuda(launch_gemm(a, c, reinterpret_cast<cudaStream_t>(stream)));
+  return status_of(launch_gemm(a, c, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 // ------------------------------------------------------------ E4M3 variant
@@ -391,7 +383,7 @@ w8a8_status w8a8_gelu(const void* h, int64_t M, int64_t K, int64_t ldh, void* g,
   DeviceInfo dev;
   w8a8_status st = current_device(&dev);
   if (st != W8A8_OK) return st;
-  return from_cuda(launch_gelu(h, M, K, ldh, g, ldg, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
+  return status_of(launch_gelu(h, M, K, ldh, g, ldg, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 w8a8_status w8a8_linear_gelu(const void* h, const int8_t* wq, const float* scale_w, const void* bias, void* out,
@@ -436,7 +428,7 @@ w8a8_status w8a8_selftest_wait_timeout(int64_t timeout_ns, w8a8_stream_t stream)
   DeviceInfo dev;
   w8a8_status st = current_device(&dev);
   if (st != W8A8_OK) return st;
-  return from_cuda(launch_selftest_wait(static_cast<uint64_t>(timeout_ns), reinterpret_cast<cudaStream_t>(stream)));
+  return status_of(launch_selftest_wait(static_cast<uint64_t>(timeout_ns), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -93,6 +93,17 @@ w8a8_status check_linear_call(const void* x, const int8_t* wq, const float* scal
                               const void* out, const void* ws_xq, const float* ws_scale_a, int64_t M, int64_t N,
                               int64_t K);
 
+// What every entry point shares: pointer alignment, CUDA launch results as
+// statuses, and whether output rows [rows][heads][dim] with these strides
+// (elements) do not overlap one another.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline w8a8_status status_of(cudaError_t e) {
+  if (e == cudaSuccess) return W8A8_OK;
+  if (e == cudaErrorInvalidValue) return W8A8_ERR_INVALID_ARG;
+  return W8A8_ERR_LAUNCH;
+}
+bool rows_disjoint(int64_t rows, int64_t ld, int64_t heads, int64_t hs, int64_t dim);
+
 // Synchronizes the current device and reads (optionally clears) the device
 // error word written by timed-out waits.
 cudaError_t read_device_error(int* value, bool clear);
