@@ -284,6 +284,12 @@ W8A8_API w8a8_status w8a8_linear_fp8(const void* x, const uint8_t* wq, const flo
                                      void* out, uint8_t* ws_xq, float* ws_scale_a,
                                      int64_t M, int64_t N, int64_t K, w8a8_stream_t stream);
 
+/* Element-wise functions: GELU in the tanh form, and silu(g) = g / (1 +
+ * exp(-g)).  As the step a chain layer applies to its input before
+ * quantizing it (NONE or GELU, see w8a8_linear_gelu), and as the gate of
+ * the gated linear layer (GELU or SILU, see w8a8_linear_glu). */
+enum { W8A8_ACT_NONE = 0, W8A8_ACT_GELU = 1, W8A8_ACT_SILU = 2 };
+
 /*
  * GELU before a linear layer, fused with its quantizer (the per-token
  * quantizer moved into the producer of X: a DiT MLP's GELU sits between the
@@ -326,6 +332,42 @@ W8A8_API w8a8_status w8a8_gelu(const void* h, int64_t M, int64_t K, int64_t ldh,
 W8A8_API w8a8_status w8a8_linear_gelu(const void* h, const int8_t* wq, const float* scale_w, const void* bias,
                                       void* out, int8_t* ws_xq, float* ws_scale_a,
                                       int64_t M, int64_t N, int64_t K, w8a8_stream_t stream);
+
+/*
+ * The gated linear layer of an MLP (the up-projection of a block whose MLP
+ * is W_down (act(W_gate x) * (W_up x))), both projections, the activation
+ * and the product in one GEMM.  Two w8a8_linear calls would write both
+ * projections to memory and a third kernel would read them back.
+ *   wq int8 [2N, K], scale_w fp32 [2N], bias bf16 [2N] or NULL: rows 0..N-1
+ *   the gate, rows N..2N-1 the projection it gates (two nn.Linear weights one
+ *   after the other);  out bf16 [M, N];  act W8A8_ACT_SILU or W8A8_ACT_GELU.
+ *     g[m,n] = (fl32(acc[m,n])   * scale_a[m]) * scale_w[n]   + bias[n]
+ *     u[m,n] = (fl32(acc[m,N+n]) * scale_a[m]) * scale_w[N+n] + bias[N+n]
+ *     out[m,n] = bf16_rne(act(g[m,n]) * u[m,n])
+ * acc, codes and scales are those of w8a8_linear (exact), g and u round after
+ * each operation as there; act is evaluated in binary32 to within 2^-15 of
+ * its value (below 2^-100 it may become 0).  M, N >= 0, N <= 2^30 - 1, N % 8 ==
+ * 0; other arguments, workspaces, alignment and errors as for w8a8_gemm(_ex),
+ * w8a8_linear and their FP8 counterparts.
+ */
+W8A8_API w8a8_status w8a8_gemm_glu(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
+                                   const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                                   w8a8_stream_t stream);
+W8A8_API w8a8_status w8a8_gemm_glu_ex(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
+                                      const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                                      const w8a8_gemm_config* cfg, w8a8_stream_t stream);
+W8A8_API w8a8_status w8a8_gemm_glu_fp8(const uint8_t* xq, const uint8_t* wq, const float* scale_a,
+                                       const float* scale_w, const void* bias, void* out, int64_t M, int64_t N,
+                                       int64_t K, int32_t act, w8a8_stream_t stream);
+W8A8_API w8a8_status w8a8_gemm_glu_fp8_ex(const uint8_t* xq, const uint8_t* wq, const float* scale_a,
+                                          const float* scale_w, const void* bias, void* out, int64_t M, int64_t N,
+                                          int64_t K, int32_t act, const w8a8_gemm_config* cfg, w8a8_stream_t stream);
+W8A8_API w8a8_status w8a8_linear_glu(const void* x, const int8_t* wq, const float* scale_w, const void* bias,
+                                     void* out, int8_t* ws_xq, float* ws_scale_a, int64_t M, int64_t N, int64_t K,
+                                     int32_t act, w8a8_stream_t stream);
+W8A8_API w8a8_status w8a8_linear_glu_fp8(const void* x, const uint8_t* wq, const float* scale_w, const void* bias,
+                                         void* out, uint8_t* ws_xq, float* ws_scale_a, int64_t M, int64_t N,
+                                         int64_t K, int32_t act, w8a8_stream_t stream);
 
 /*
  * Norms of queries and keys with the position rotation, in one pass over the
@@ -398,9 +440,6 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  * copies.  The chain holds no device memory.  Calls that launch the same
  * chain (or chains sharing buffers) must not overlap on the GPU.
  */
-/* Element-wise step a chain layer applies to its input before quantizing
- * it (see w8a8_linear_gelu). */
-enum { W8A8_ACT_NONE = 0, W8A8_ACT_GELU = 1 };
 
 typedef struct {
     const void* x;            /* bf16 [M, K] input (row stride K) */
@@ -412,7 +451,8 @@ typedef struct {
     float* ws_scale_a;        /* fp32 [M] workspace */
     int64_t M, N, K;
     int32_t input_act;        /* W8A8_ACT_NONE, or W8A8_ACT_GELU: the layer computes GELU(x) W^T + b */
-    int32_t reserved;         /* zero */
+    int32_t output_glu;       /* W8A8_ACT_NONE, or a gate (W8A8_ACT_SILU, W8A8_ACT_GELU): the layer is
+                                 w8a8_linear_glu, with wq, scale_w and bias of 2N rows; input_act is then NONE */
 } w8a8_linear_desc;
 
 typedef struct w8a8_chain_st* w8a8_chain_t;

@@ -42,3 +42,39 @@ def test_qk_norm_rope(w8, change, status):
 
 def test_qk_norm_rope_needs_arguments(w8):
     assert w8.raw_lib().w8a8_qk_norm_rope(None, None) == 1
+
+
+def glu(w8, fn="w8a8_linear_glu", M=4, N=8, K=32, act=2, x=A, wq=A, sw=A, bias=None, out=A, xq=A, sa=A):
+    return getattr(w8.raw_lib(), fn)(x, wq, sw, bias, out, xq, sa, M, N, K, act, None)
+
+
+@pytest.mark.parametrize("fn", ["w8a8_linear_glu", "w8a8_linear_glu_fp8"])
+@pytest.mark.parametrize("change,status", [
+    (dict(act=0), 1), (dict(act=3), 1), (dict(act=0, M=0), 1), (dict(N=12), 1), (dict(K=24), 1), (dict(M=-1), 1),
+    (dict(N=2 ** 30), 1), (dict(x=None), 1), (dict(sw=None), 1), (dict(sa=None), 1), (dict(out=None), 1),
+    (dict(wq=A + 8), 2), (dict(bias=A + 2), 2), (dict(xq=A + 4), 2), (dict(M=0), 0), (dict(N=0, act=1), 0),
+])
+def test_linear_glu(w8, fn, change, status):
+    assert glu(w8, fn, **change) == status
+
+
+@pytest.mark.parametrize("fn", ["w8a8_gemm_glu", "w8a8_gemm_glu_fp8"])
+def test_gemm_glu(w8, fn):
+    call = getattr(w8.raw_lib(), fn)
+    assert call(A, A, A, A, None, A, 4, 8, 32, 0, None) == 1
+    assert call(A, A, None, A, None, A, 4, 8, 32, 2, None) == 1
+    assert call(A, A, A, None, None, A, 4, 8, 32, 2, None) == 1
+    assert call(A, A, A, A, None, A, 4, 2 ** 30, 32, 2, None) == 1
+    assert call(A, A, A, A, A + 2, A, 4, 8, 32, 1, None) == 2
+    assert call(A, A, A, A, None, A, 0, 8, 32, 1, None) == 0
+    cfg = w8.GemmConfig(block_m=256, block_n=256, stages=7, grid=2, raster_group=1)
+    assert getattr(w8.raw_lib(), fn + "_ex")(A, A, A, A, None, A, 4, 8, 32, 2, ctypes.byref(cfg), None) == 1
+
+
+def test_chain_with_gated_layers(w8):
+    h = ctypes.c_void_p(None)
+    for extra in ((0, 3), (1, 2), (0, -1)):  # (input_act, output_glu): unknown gates, GELU before a gated layer
+        d = (w8.LinearDesc * 1)(w8.LinearDesc(A, A, A, None, A, A, A, 4, 8, 32, *extra))
+        assert w8.raw_lib().w8a8_chain_create(d, 1, ctypes.byref(h)) == 1 and not h.value
+    d = (w8.LinearDesc * 1)(w8.LinearDesc(A, A, A, None, A, A + 4, A, 4, 8, 32, 0, 2))
+    assert w8.raw_lib().w8a8_chain_create(d, 1, ctypes.byref(h)) == 2 and not h.value

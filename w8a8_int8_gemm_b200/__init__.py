@@ -30,7 +30,9 @@ __all__ = [
     "w8a8_linear_noalloc",
     "w8a8_quantize_act_fp8", "w8a8_quantize_weight_fp8", "w8a8_gemm_fp8", "w8a8_gemm_fp8_ex",
     "w8a8_gemm_fp8_f32", "w8a8_gemm_fp8_f32_ex", "w8a8_linear_fp8",
-    "w8a8_quantize_act_gelu", "w8a8_gelu", "w8a8_linear_gelu", "ACT_NONE", "ACT_GELU",
+    "w8a8_quantize_act_gelu", "w8a8_gelu", "w8a8_linear_gelu", "ACT_NONE", "ACT_GELU", "ACT_SILU",
+    "w8a8_gemm_glu", "w8a8_gemm_glu_ex", "w8a8_gemm_glu_fp8", "w8a8_gemm_glu_fp8_ex", "w8a8_linear_glu",
+    "w8a8_linear_glu_fp8",
     "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS",
     "LinearDesc", "Chain", "linear_layer", "w8a8_chain_create", "w8a8_chain_launch", "w8a8_chain_layers",
     "w8a8_chain_destroy",
@@ -46,6 +48,7 @@ W8A8_OK = 0
 W8A8_ERR_TIMEOUT = 5
 ACT_NONE = 0   # W8A8_ACT_NONE
 ACT_GELU = 1   # W8A8_ACT_GELU
+ACT_SILU = 2   # W8A8_ACT_SILU
 ROPE_HALVES = 0  # W8A8_ROPE_HALVES
 ROPE_PAIRS = 1   # W8A8_ROPE_PAIRS
 
@@ -70,7 +73,7 @@ class LinearDesc(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("scale_w", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p), ("ws_xq", ctypes.c_void_p),
                 ("ws_scale_a", ctypes.c_void_p), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
-                ("K", ctypes.c_int64), ("input_act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("K", ctypes.c_int64), ("input_act", ctypes.c_int32), ("output_glu", ctypes.c_int32)]
 
 
 class QkDesc(ctypes.Structure):
@@ -113,6 +116,13 @@ def _load() -> ctypes.CDLL:
         "w8a8_quantize_act_gelu": ([p, i64, i64, i64, p, i64, p, p], ctypes.c_int),
         "w8a8_gelu": ([p, i64, i64, i64, p, i64, p], ctypes.c_int),
         "w8a8_linear_gelu": ([p, p, p, p, p, p, p, i64, i64, i64, p], ctypes.c_int),
+        "w8a8_gemm_glu": ([p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
+        "w8a8_gemm_glu_ex": ([p, p, p, p, p, p, i64, i64, i64, i32, ctypes.POINTER(GemmConfig), p], ctypes.c_int),
+        "w8a8_gemm_glu_fp8": ([p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
+        "w8a8_gemm_glu_fp8_ex": ([p, p, p, p, p, p, i64, i64, i64, i32, ctypes.POINTER(GemmConfig), p],
+                                 ctypes.c_int),
+        "w8a8_linear_glu": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
+        "w8a8_linear_glu_fp8": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
         "w8a8_qk_norm_rope": ([ctypes.POINTER(QkDesc), p], ctypes.c_int),
         "w8a8_chain_create": ([ctypes.POINTER(LinearDesc), i32, ctypes.POINTER(p)], ctypes.c_int),
         "w8a8_chain_launch": ([p, p], ctypes.c_int),
@@ -557,6 +567,101 @@ def w8a8_linear_gelu(h, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a
     return l["out"]
 
 
+# ------------------------------------------------- the gated linear layer
+
+
+def _gemm_glu(fn, what, code, xq, wq, scale_a, scale_w, bias, out, act, config, stream):
+    _need(xq, "xq", code, 2)
+    M, K = xq.shape
+    _need_contig(xq, "xq", code, (M, K))
+    N = _glu_weight(wq, code, K, scale_w, bias)
+    _need_contig(scale_a, "scale_a", torch.float32, (M,))
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+    _need_contig(out, "out", torch.bfloat16, (M, N))
+    dev = _one_device(xq, wq, scale_a, scale_w, bias, out)
+    c = _cfg(config)
+    with torch.cuda.device(dev):
+        _check(fn(_ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K, int(act),
+                  ctypes.byref(c) if c is not None else None, _stream(stream, dev)), what)
+    return out
+
+
+def _glu_weight(wq, code, K, scale_w, bias) -> int:
+    """Checks the weight of a gated layer, [2N, K] with its scales and bias; N."""
+    _need(wq, "wq", code, 2)
+    if wq.shape[0] % 2:
+        raise ValueError(f"wq must have an even number of rows (gate, then up), got {wq.shape[0]}")
+    if wq.shape[1] != K:
+        raise ValueError(f"inner dimensions differ: the activations have K={K}, wq has K={wq.shape[1]}")
+    rows = wq.shape[0]
+    _need_contig(wq, "wq", code, (rows, K))
+    _need_contig(scale_w, "scale_w", torch.float32, (rows,))
+    if bias is not None:
+        _need_contig(bias, "bias", torch.bfloat16, (rows,))
+    return rows // 2
+
+
+def w8a8_gemm_glu_ex(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = ACT_SILU, config=None, stream=None):
+    """w8a8_gemm_glu with an explicit tile configuration (None = selected per shape)."""
+    return _gemm_glu(_lib.w8a8_gemm_glu_ex, "w8a8_gemm_glu_ex", torch.int8, xq, wq, scale_a, scale_w, bias, out, act,
+                     config, stream)
+
+
+def w8a8_gemm_glu(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = ACT_SILU, stream=None):
+    """out bf16 [M, N] = act(g) * u, with g and u the dequantized and biased products of xq int8 [M, K] with
+    rows 0..N-1 and N..2N-1 of wq int8 [2N, K]; act ACT_SILU or ACT_GELU."""
+    return w8a8_gemm_glu_ex(xq, wq, scale_a, scale_w, bias, out, act, None, stream)
+
+
+def w8a8_gemm_glu_fp8_ex(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = ACT_SILU, config=None,
+                         stream=None):
+    """w8a8_gemm_glu_fp8 with an explicit tile configuration (None = selected per shape)."""
+    return _gemm_glu(_lib.w8a8_gemm_glu_fp8_ex, "w8a8_gemm_glu_fp8_ex", torch.uint8, xq, wq, scale_a, scale_w, bias,
+                     out, act, config, stream)
+
+
+def w8a8_gemm_glu_fp8(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = ACT_SILU, stream=None):
+    """w8a8_gemm_glu on E4M3 codes (torch.uint8)."""
+    return w8a8_gemm_glu_fp8_ex(xq, wq, scale_a, scale_w, bias, out, act, None, stream)
+
+
+def _linear_glu(fn, what, code, x, wq, scale_w, bias, out, act, ws_xq, ws_scale_a, stream):
+    _need(x, "x", torch.bfloat16, 2)
+    M, K = x.shape
+    _need_contig(x, "x", torch.bfloat16, (M, K))
+    N = _glu_weight(wq, code, K, scale_w, bias)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    if ws_xq is None:
+        ws_xq = torch.empty((M, K), dtype=code, device=x.device)
+    if ws_scale_a is None:
+        ws_scale_a = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need_contig(out, "out", torch.bfloat16, (M, N))
+    _need_contig(ws_xq, "ws_xq", code, (M, K))
+    _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
+    dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
+    with torch.cuda.device(dev):
+        _check(fn(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq), _ptr(ws_scale_a), M, N, K,
+                  int(act), _stream(stream, dev)), what)
+    return out
+
+
+def w8a8_linear_glu(x, wq, scale_w, bias=None, out=None, act: int = ACT_SILU, ws_xq=None, ws_scale_a=None,
+                    stream=None):
+    """The gated linear layer of an MLP: out bf16 [M, N] = act(x Wg^T + bg) * (x Wu^T + bu) from bf16 x [M, K]
+    and int8 wq [2N, K] (gate rows, then up rows); workspaces as in w8a8_linear."""
+    return _linear_glu(_lib.w8a8_linear_glu, "w8a8_linear_glu", torch.int8, x, wq, scale_w, bias, out, act, ws_xq,
+                       ws_scale_a, stream)
+
+
+def w8a8_linear_glu_fp8(x, wq, scale_w, bias=None, out=None, act: int = ACT_SILU, ws_xq=None, ws_scale_a=None,
+                        stream=None):
+    """w8a8_linear_glu with E4M3 codes (wq and ws_xq torch.uint8)."""
+    return _linear_glu(_lib.w8a8_linear_glu_fp8, "w8a8_linear_glu_fp8", torch.uint8, x, wq, scale_w, bias, out, act,
+                       ws_xq, ws_scale_a, stream)
+
+
 # ------------------------------------------------- between QKV and attention
 
 
@@ -622,13 +727,19 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
 # ------------------------------------------------- chains of linear layers
 
 
-def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=None, input_act: int = ACT_NONE) -> dict:
+def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=None, input_act: int = ACT_NONE,
+                 output_glu: int = ACT_NONE) -> dict:
     """One layer of a chain: the tensors of a w8a8_linear call, with the
     output and workspace allocated here when not given.  x may be an
     earlier layer's ``out``; input_act=ACT_GELU makes the layer compute
-    GELU(x) W^T + b (w8a8_linear_gelu)."""
+    GELU(x) W^T + b (w8a8_linear_gelu); output_glu=ACT_SILU or ACT_GELU
+    makes it a gated one (w8a8_linear_glu), with wq [2N, K]."""
     _need(x, "x", torch.bfloat16, 2)
     M, K = x.shape
+    if output_glu != ACT_NONE:
+        _need_contig(x, "x", torch.bfloat16, (M, K))
+        N = _glu_weight(wq, torch.int8, K, scale_w, bias)
+        return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu)
     _need(wq, "wq", torch.int8, 2)
     N = wq.shape[0]
     if wq.shape[1] != K:
@@ -638,6 +749,10 @@ def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=Non
     _need_contig(scale_w, "scale_w", torch.float32, (N,))
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
+    return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, ACT_NONE)
+
+
+def _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu) -> dict:
     dev = x.device
     out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
     ws_xq = torch.empty((M, K), dtype=torch.int8, device=dev) if ws_xq is None else ws_xq
@@ -646,7 +761,8 @@ def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=Non
     _need_contig(ws_xq, "ws_xq", torch.int8, (M, K))
     _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
     return {"x": x, "wq": wq, "scale_w": scale_w, "bias": bias, "out": out, "ws_xq": ws_xq,
-            "ws_scale_a": ws_scale_a, "M": M, "N": N, "K": K, "input_act": int(input_act)}
+            "ws_scale_a": ws_scale_a, "M": M, "N": N, "K": K, "input_act": int(input_act),
+            "output_glu": int(output_glu)}
 
 
 class Chain:
@@ -686,7 +802,7 @@ def w8a8_chain_create(layers: list) -> Chain:
     for i, l in enumerate(layers):
         descs[i] = LinearDesc(_ptr(l["x"]), _ptr(l["wq"]), _ptr(l["scale_w"]), _ptr(l.get("bias")), _ptr(l["out"]),
                               _ptr(l["ws_xq"]), _ptr(l["ws_scale_a"]), l["M"], l["N"], l["K"],
-                              int(l.get("input_act", ACT_NONE)), 0)
+                              int(l.get("input_act", ACT_NONE)), int(l.get("output_glu", ACT_NONE)))
     h = ctypes.c_void_p(None)
     _check(_lib.w8a8_chain_create(descs, len(layers), ctypes.byref(h)), "w8a8_chain_create")
     return Chain(h.value, list(layers))

@@ -61,6 +61,12 @@ w8a8_status check_gemm_shape(int64_t M, int64_t N, int64_t K) {
   return W8A8_OK;
 }
 
+// The gated layer: a known activation, and 2 N rows of weights that fit the row type.
+w8a8_status check_glu(int64_t N, int32_t act) {
+  if (act != W8A8_ACT_SILU && act != W8A8_ACT_GELU) return W8A8_ERR_INVALID_ARG;
+  return N > kMaxMN / 2 ? W8A8_ERR_INVALID_ARG : W8A8_OK;
+}
+
 w8a8_status check_config(const w8a8_gemm_config& c) {
   if (c.block_m != 128 && c.block_m != 256) return W8A8_ERR_INVALID_ARG;
   if (c.block_n != 128 && c.block_n != 256) return W8A8_ERR_INVALID_ARG;
@@ -120,21 +126,24 @@ w8a8_gemm_config select(int64_t M, int64_t N, int64_t K, int sms, bool allow_pai
 w8a8_status gemm_common(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
                         const void* bias, void* out, int64_t M, int64_t N, int64_t K,
                         const w8a8_gemm_config* user_cfg, GemmOut kind, cudaStream_t stream,
-                        bool overlap_prologue = false, GemmElem elem = GemmElem::kInt8) {
+                        bool overlap_prologue = false, GemmElem elem = GemmElem::kInt8, int32_t act = 0) {
   w8a8_status st = check_gemm_shape(M, N, K);
   if (st != W8A8_OK) return st;
+  if (kind == GemmOut::kGlu && (st = check_glu(N, act)) != W8A8_OK) return st;
   if (user_cfg != nullptr && (st = check_config(*user_cfg)) != W8A8_OK) return st;
   if (M == 0 || N == 0) return W8A8_OK;
   if (xq == nullptr || wq == nullptr || out == nullptr) return W8A8_ERR_INVALID_ARG;
-  if (kind == GemmOut::kBf16Dequant && (scale_a == nullptr || scale_w == nullptr)) return W8A8_ERR_INVALID_ARG;
+  if (kind != GemmOut::kAcc32 && (scale_a == nullptr || scale_w == nullptr)) return W8A8_ERR_INVALID_ARG;
   if (!aligned16(xq) || !aligned16(wq) || !aligned16(out) || !aligned16(scale_a) || !aligned16(scale_w) ||
       !aligned16(bias)) {
     return W8A8_ERR_ALIGNMENT;
   }
   DeviceInfo dev;
   if ((st = current_device(&dev)) != W8A8_OK) return st;
-  const w8a8_gemm_config cfg = user_cfg ? *user_cfg : select(M, N, K, dev.sms);
+  // (the gated layer's product has the columns of both projections)
+  const w8a8_gemm_config cfg = user_cfg ? *user_cfg : select(M, kind == GemmOut::kGlu ? 2 * N : N, K, dev.sms);
   GemmArgs a;
+  a.act = act;
   a.xq = xq;
   a.wq = wq;
   a.scale_a = scale_a;
@@ -207,6 +216,13 @@ w8a8_status check_linear_call(const void* x, const int8_t* wq, const float* scal
   if (ws_xq == nullptr || ws_scale_a == nullptr) return W8A8_ERR_INVALID_ARG;
   if (!aligned16(ws_xq) || !aligned16(ws_scale_a)) return W8A8_ERR_ALIGNMENT;
   return W8A8_OK;
+}
+
+w8a8_status check_glu_call(const void* x, const int8_t* wq, const float* scale_w, const void* bias, const void* out,
+                           const void* ws_xq, const float* ws_scale_a, int64_t M, int64_t N, int64_t K, int32_t act) {
+  w8a8_status st = check_gemm_shape(M, N, K);
+  if (st == W8A8_OK) st = check_glu(N, act);
+  return st != W8A8_OK ? st : check_linear_call(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K);
 }
 
 // W8A8_OK if the current device is supported (sm_100), from the cached
@@ -395,6 +411,59 @@ w8a8_status w8a8_linear_gelu(const void* h, const int8_t* wq, const float* scale
   if (st != W8A8_OK) return st;
   return gemm_common(ws_xq, wq, ws_scale_a, scale_w, bias, out, M, N, K, nullptr, GemmOut::kBf16Dequant,
                      reinterpret_cast<cudaStream_t>(stream), /*overlap_prologue=*/true);
+}
+
+// ------------------------------------------------- the gated linear layer
+
+w8a8_status w8a8_gemm_glu_ex(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
+                             const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                             const w8a8_gemm_config* cfg, w8a8_stream_t stream) {
+  return gemm_common(xq, wq, scale_a, scale_w, bias, out, M, N, K, cfg, GemmOut::kGlu,
+                     reinterpret_cast<cudaStream_t>(stream), /*overlap_prologue=*/false, GemmElem::kInt8, act);
+}
+
+w8a8_status w8a8_gemm_glu(const int8_t* xq, const int8_t* wq, const float* scale_a, const float* scale_w,
+                          const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                          w8a8_stream_t stream) {
+  return w8a8_gemm_glu_ex(xq, wq, scale_a, scale_w, bias, out, M, N, K, act, nullptr, stream);
+}
+
+w8a8_status w8a8_gemm_glu_fp8_ex(const uint8_t* xq, const uint8_t* wq, const float* scale_a, const float* scale_w,
+                                 const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                                 const w8a8_gemm_config* cfg, w8a8_stream_t stream) {
+  return gemm_common(reinterpret_cast<const int8_t*>(xq), reinterpret_cast<const int8_t*>(wq), scale_a, scale_w,
+                     bias, out, M, N, K, cfg, GemmOut::kGlu, reinterpret_cast<cudaStream_t>(stream),
+                     /*overlap_prologue=*/false, GemmElem::kE4M3, act);
+}
+
+w8a8_status w8a8_gemm_glu_fp8(const uint8_t* xq, const uint8_t* wq, const float* scale_a, const float* scale_w,
+                              const void* bias, void* out, int64_t M, int64_t N, int64_t K, int32_t act,
+                              w8a8_stream_t stream) {
+  return w8a8_gemm_glu_fp8_ex(xq, wq, scale_a, scale_w, bias, out, M, N, K, act, nullptr, stream);
+}
+
+w8a8_status w8a8_linear_glu(const void* x, const int8_t* wq, const float* scale_w, const void* bias, void* out,
+                            int8_t* ws_xq, float* ws_scale_a, int64_t M, int64_t N, int64_t K, int32_t act,
+                            w8a8_stream_t stream) {
+  w8a8_status st = check_glu_call(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, act);
+  if (st != W8A8_OK || M == 0 || N == 0) return st;
+  st = w8a8_quantize_act(x, M, K, K, ws_xq, K, ws_scale_a, stream);
+  if (st != W8A8_OK) return st;
+  return gemm_common(ws_xq, wq, ws_scale_a, scale_w, bias, out, M, N, K, nullptr, GemmOut::kGlu,
+                     reinterpret_cast<cudaStream_t>(stream), /*overlap_prologue=*/true, GemmElem::kInt8, act);
+}
+
+w8a8_status w8a8_linear_glu_fp8(const void* x, const uint8_t* wq, const float* scale_w, const void* bias, void* out,
+                                uint8_t* ws_xq, float* ws_scale_a, int64_t M, int64_t N, int64_t K, int32_t act,
+                                w8a8_stream_t stream) {
+  const int8_t* w = reinterpret_cast<const int8_t*>(wq);
+  w8a8_status st = check_glu_call(x, w, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, act);
+  if (st != W8A8_OK || M == 0 || N == 0) return st;
+  st = w8a8_quantize_act_fp8(x, M, K, K, ws_xq, K, ws_scale_a, stream);
+  if (st != W8A8_OK) return st;
+  return gemm_common(reinterpret_cast<const int8_t*>(ws_xq), w, ws_scale_a, scale_w, bias, out, M, N, K, nullptr,
+                     GemmOut::kGlu, reinterpret_cast<cudaStream_t>(stream), /*overlap_prologue=*/true,
+                     GemmElem::kE4M3, act);
 }
 
 int64_t w8a8_linear_sync_words(int64_t M) { return M < 0 ? 0 : linear_sync_words(M); }

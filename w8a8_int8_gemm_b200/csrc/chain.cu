@@ -13,7 +13,8 @@
 // A layer's input may be an earlier layer's output (same buffer): the
 // graph keeps the stream order of the calls, so the later quantizer reads
 // the finished output.  A layer may apply GELU to its input on the way into
-// its quantizer (the producer of the input fused with the quantizer).  The
+// its quantizer (the producer of the input fused with the quantizer), or be
+// a gated one (w8a8_linear_glu).  The
 // runner owns no device memory: every buffer is the caller's and must
 // outlive the chain.
 #include <cuda_runtime.h>
@@ -36,6 +37,10 @@ namespace {
 // The checks w8a8_linear makes, before any CUDA call, and the layer's input step.
 w8a8_status check_layer(const w8a8_linear_desc& l) {
   if (l.input_act != W8A8_ACT_NONE && l.input_act != W8A8_ACT_GELU) return W8A8_ERR_INVALID_ARG;
+  if (l.output_glu != W8A8_ACT_NONE) {
+    return w8a8::check_glu_call(l.x, l.wq, l.scale_w, l.bias, l.out, l.ws_xq, l.ws_scale_a, l.M, l.N, l.K,
+                                l.input_act == W8A8_ACT_NONE ? l.output_glu : -1);
+  }
   return w8a8::check_linear_call(l.x, l.wq, l.scale_w, l.bias, l.out, l.ws_xq, l.ws_scale_a, l.M, l.N, l.K);
 }
 
@@ -77,6 +82,11 @@ w8a8_status w8a8_chain_create(const w8a8_linear_desc* layers, int32_t count, w8a
   }
   for (int32_t i = 0; i < count && st == W8A8_OK; ++i) {
     const w8a8_linear_desc& l = layers[i];
+    if (l.output_glu != W8A8_ACT_NONE) {
+      st = w8a8_linear_glu(l.x, l.wq, l.scale_w, l.bias, l.out, l.ws_xq, l.ws_scale_a, l.M, l.N, l.K, l.output_glu,
+                           reinterpret_cast<w8a8_stream_t>(s));
+      continue;
+    }
     auto linear = l.input_act == W8A8_ACT_GELU ? w8a8_linear_gelu : w8a8_linear;
     st = linear(l.x, l.wq, l.scale_w, l.bias, l.out, l.ws_xq, l.ws_scale_a, l.M, l.N, l.K,
                 reinterpret_cast<w8a8_stream_t>(s));

@@ -40,6 +40,19 @@
 // instruction, so the tiles, the ring and the swizzle are unchanged; the
 // accumulators are fp32 and the epilogue uses them as they are.
 //
+// And the gated layer (OUT = kGlu): W holds two projections, N gate rows and
+// N rows of the other, and
+//   out[m,n] = bf16_rne(act(g) * u),   g, u = the dequantized and biased
+//   sums of columns n and N + n,       act = SiLU or GELU (tanh form).
+// A tile's BN accumulator columns are BN/2 gate columns and the BN/2 columns
+// they gate, so both meet in one epilogue warp and neither projection goes
+// to memory: per token 4N bytes written and 4N read back less than two
+// linear layers and a gating kernel.  W keeps its plain layout: the operand
+// tile is two boxes of BN/2 rows, N rows apart (in a CTA pair each CTA loads
+// one of them anyway).  The MMAs bound it, as they bound the plain layer: the
+// gate's exponential and division, two special-function operations per
+// output, run in the epilogue warps beside the next tile's MMAs.
+//
 // Every mbarrier wait is bounded in time (see sm100_ptx.cuh); on timeout the
 // kernel records the site in the device error word, lets its in-flight
 // copies and MMAs finish (again bounded), frees tensor memory and exits.
@@ -90,6 +103,7 @@ struct Params {
   // more than half of L2 (long-K layers: A is then streamed once per tile
   // row and would push B out, which every tile row reads again).
   int a_evict_first;
+  int gelu;  // kGlu: the gate's activation (GELU, else SiLU)
   // Fused linear layer only: the bf16 activations, the workspace the kernel
   // quantizes them into (xq is also the A operand of tm_a), and the
   // row-block counters ([m_tiles] blocks + 1 CTA counter, zero on entry).
@@ -173,6 +187,45 @@ __device__ __forceinline__ void dequant_32(const uint32_t (&v)[32], float sa, co
   }
 }
 
+// The gate of kGlu: g * sigmoid(g) (SiLU) or g * sigmoid(2 sqrt(2/pi) (g +
+// 0.044715 g^3)) (the tanh form of GELU, without its cancellation).  The
+// exponential's argument is rounded in binary32: a relative error below
+// 2^-16 of the result over the whole range, far inside the bf16 rounding.
+__device__ __forceinline__ float glu_gate(float g, bool gelu) {
+  const float a = gelu ? 1.5957691216f * fmaf(0.044715f * g * g, g, g) : g;
+  return __fdividef(g, 1.0f + __expf(-a));
+}
+
+// 32 gate and 32 gated accumulators of one row -> 16 packed bf16 pairs:
+// both dequantized as in dequant_32 (each operation rounded), then
+// act(g) * u with the one rounding to bf16.
+template <bool kF32Acc>
+__device__ __forceinline__ void glu_32(const uint32_t (&vg)[32], const uint32_t (&vu)[32], float sa, const float* sw_g,
+                                       const float* sw_u, const uint16_t* b_g, const uint16_t* b_u, bool gelu,
+                                       uint32_t* packed) {
+  auto dequant = [&](uint32_t a, float sw, uint16_t bias) {
+    float t = kF32Acc ? __uint_as_float(a) : __int2float_rn(static_cast<int>(a));
+    t = __fmul_rn(t, sa);
+    t = __fmul_rn(t, sw);
+    return __fadd_rn(t, __uint_as_float(static_cast<uint32_t>(bias) << 16));
+  };
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float4 sg = *reinterpret_cast<const float4*>(sw_g + 4 * q);
+    const float4 su = *reinterpret_cast<const float4*>(sw_u + 4 * q);
+    const ushort4 bg = *reinterpret_cast<const ushort4*>(b_g + 4 * q);
+    const ushort4 bu = *reinterpret_cast<const ushort4*>(b_u + 4 * q);
+    float y[4];
+    y[0] = glu_gate(dequant(vg[4 * q], sg.x, bg.x), gelu) * dequant(vu[4 * q], su.x, bu.x);
+    y[1] = glu_gate(dequant(vg[4 * q + 1], sg.y, bg.y), gelu) * dequant(vu[4 * q + 1], su.y, bu.y);
+    y[2] = glu_gate(dequant(vg[4 * q + 2], sg.z, bg.z), gelu) * dequant(vu[4 * q + 2], su.z, bu.z);
+    y[3] = glu_gate(dequant(vg[4 * q + 3], sg.w, bg.w), gelu) * dequant(vu[4 * q + 3], su.w, bu.w);
+    const __nv_bfloat162 h0 = __floats2bfloat162_rn(y[0], y[1]), h1 = __floats2bfloat162_rn(y[2], y[3]);
+    packed[2 * q] = *reinterpret_cast<const uint32_t*>(&h0);
+    packed[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+  }
+}
+
 // One kernel for both tile shapes.  PAIR = false: one CTA computes a
 // 128 x BN tile.  PAIR = true: a cluster of two CTAs computes a 256 x BN tile
 // with tcgen05 cta_group::2 -- each CTA loads its own 128 rows of A and half
@@ -207,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kTxBytes = (PAIR ? 2 : 1) * (kA + kB);
   constexpr uint32_t kTmemCols = 2 * BN;  // two accumulator buffers; 256 or 512 (power of two)
   constexpr bool kE4M3 = EL == GemmElem::kE4M3;
+  constexpr bool kGlu = OUT == GemmOut::kGlu;
   constexpr uint32_t kIdesc = kE4M3 ? make_idesc_e4m3(kTileM, BN) : make_idesc_i8(kTileM, BN);
   // half-width tail items
   constexpr uint32_t kIdescHalf = kE4M3 ? make_idesc_e4m3(kTileM, BN / 2) : make_idesc_i8(kTileM, BN / 2);
@@ -290,8 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int a_row = mb * kTileM + static_cast<int>(rank) * kBlockM;
       // this CTA's rows of B: all BN (single CTA) or its half (pair); a
       // half-width item covers BN / 2 columns, of which a pair's CTA loads half
-      const int b_row = nb * BN + (hb < 0 ? static_cast<int>(rank) * kBRows
-                                          : hb * (BN / 2) + static_cast<int>(rank) * (kBRows / 2));
+      // (gated layer: BN / 2 output columns per tile; a pair's leader loads their gate rows and its peer the
+      // rows N further on, a single CTA both in two boxes; rows past N in the gate's box are the other
+      // projection's and only reach columns that are not stored)
+      const int b_row =
+          kGlu ? nb * (BN / 2) + (hb < 0 ? 0 : hb * (BN / 4)) + static_cast<int>(rank) * p.N
+               : nb * BN + (hb < 0 ? static_cast<int>(rank) * kBRows
+                                   : hb * (BN / 2) + static_cast<int>(rank) * (kBRows / 2));
       // a half-width item loads half of B's rows, through the tensor map with half-height boxes
       const CUtensorMap* map_b = hb < 0 ? &tm_b : &tm_b_half;
       const uint32_t tx_bytes = hb < 0 ? kTxBytes : (PAIR ? 2u : 1u) * (kA + kB / 2);
@@ -314,7 +373,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair_hint(sA + stage * kA, &tm_a, bar, kb * kBlockK, a_row, a_pol);
           } else {
             mbar_arrive_expect_tx(&full[stage], tx_bytes);
-            tma_load_2d_hint(sB + stage * kB, map_b, &full[stage], kb * kBlockK, b_row, keep);
+            if constexpr (kGlu) {
+              tma_load_2d_hint(sB + stage * kB, &tm_b_half, &full[stage], kb * kBlockK, b_row, keep);
+              tma_load_2d_hint(sB + stage * kB + kB / 2, &tm_b_half, &full[stage], kb * kBlockK, p.N + b_row, keep);
+            } else {
+              tma_load_2d_hint(sB + stage * kB, map_b, &full[stage], kb * kBlockK, b_row, keep);
+            }
             if constexpr (!FUSE) {
               if (fills == 0) pdl_wait_prerequisites();  // A may be written by the kernel before this one
               tma_load_2d_hint(sA + stage * kA, &tm_a, &full[stage], kb * kBlockK, a_row, a_pol);
@@ -519,6 +583,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
+      if constexpr (kGlu) {
+        if (row < p.M) sa = __ldg(p.scale_a + row);
+        // scale_w and bias of the gate's columns, then of the columns they gate
+        const int out_n = tile_n / 2;
+        named_barrier_sync(1, 32 * kEpiWarps);
+        for (int i = e * 32 + lane; i < tile_n; i += 32 * kEpiWarps) {
+          const bool up = i >= out_n;
+          const int col = col_base / 2 + (up ? i - out_n : i);
+          const int n = up ? p.N + col : col;
+          ps_w[i] = col < p.N ? __ldg(p.scale_w + n) : 0.0f;
+          ps_b[i] = (col < p.N && p.bias != nullptr) ? __bfloat16_as_ushort(p.bias[n]) : static_cast<uint16_t>(0);
+        }
+        named_barrier_sync(1, 32 * kEpiWarps);
+        // This warp's half of the output columns, 32 at a time.
+        const int n_out_sub = out_n / 64;
+        const uint32_t t_gate = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                static_cast<uint32_t>(buf * BN + half * (out_n / 2));
+#pragma unroll
+        for (int sc = 0; sc < BN / 128; ++sc) {
+          if (sc >= n_out_sub) break;
+          uint32_t vg[32], vu[32];
+          tmem_load_32cols_async(t_gate + 32 * sc, vg);
+          tmem_load_32cols_async(t_gate + out_n + 32 * sc, vu);
+          tmem_wait_load(vg);
+          tmem_wait_load(vu);
+          if (sc + 1 == n_out_sub) {
+            // The last load of this accumulator buffer has completed.
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+              if (PAIR && !leader) {
+                mbar_arrive_cluster(map_to_cta(smem_u32(&tempty[buf]), 0u));
+              } else {
+                mbar_arrive(&tempty[buf]);
+              }
+            }
+          }
+          const int cl = half * (out_n / 2) + 32 * sc;
+          const int col0 = col_base / 2 + cl;
+          if (row0 < p.M && col0 < p.N) {
+            uint32_t pk[16];
+            glu_32<kE4M3>(vg, vu, sa, ps_w + cl, ps_w + out_n + cl, ps_b + cl, ps_b + out_n + cl, p.gelu != 0, pk);
+            // Two staging blocks of 32 rows x 64 bytes in turn (64-byte swizzle).
+            uint8_t* block = sbuf + (sc & 1) * (kEpiBufBytes / 2);
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int pos = j ^ ((lane >> 1) & 3);
+              *reinterpret_cast<uint4*>(block + lane * 64 + pos * 16) =
+                  make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d_hint(&tm_d, block, col0, row0, stream_out);
+              bulk_commit_group();
+            }
+            __syncwarp();
+          }
+        }
+        continue;
+      }
       if constexpr (OUT == GemmOut::kBf16Dequant) {
         if (row < p.M) sa = FUSE ? p.scale_out[row] : __ldg(p.scale_a + row);
         // This tile's scale_w and bias, staged once for all epilogue warps
@@ -681,9 +808,9 @@ EncodeTiledFn get_encode_fn() {
 }
 
 // 2-D row-major tensor [rows, cols] of `elem` bytes, box [box_rows, box_cols],
-// 128-byte swizzle, zero fill outside the tensor.
+// 128-byte swizzle unless another is named, zero fill outside the tensor.
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, int elem, const void* base, int64_t rows,
-               int64_t cols, int box_rows, int box_cols) {
+               int64_t cols, int box_rows, int box_cols, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
@@ -691,7 +818,7 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, int elem, const void
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = fn(map, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -716,6 +843,9 @@ template <int BN, GemmOut OUT, bool PAIR, bool FUSE, GemmElem EL = GemmElem::kIn
 cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t stream) {
   static_assert(!(FUSE && PAIR), "the fused linear layer runs on single CTAs");
   static_assert(!(FUSE && EL == GemmElem::kE4M3), "the fused linear layer is int8 only");
+  constexpr bool kGlu = OUT == GemmOut::kGlu;
+  static_assert(!(FUSE && kGlu), "the fused linear layer has no gate");
+  const int64_t w_rows = kGlu ? 2 * a.N : a.N;
   constexpr int kTileM = PAIR ? 2 * kBlockM : kBlockM;
   constexpr int kBRows = PAIR ? BN / 2 : BN;
   CUtensorMap tm_a, tm_b, tm_b_half, tm_d;
@@ -725,15 +855,17 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   std::memset(&tm_d, 0, sizeof tm_d);
   bool ok;
   if constexpr (KCH == 2) {
-    ok = encode_chunks(&tm_a, a.xq, a.M, a.K, kBlockM) && encode_chunks(&tm_b, a.wq, a.N, a.K, kBRows) &&
-         encode_chunks(&tm_b_half, a.wq, a.N, a.K, kBRows / 2);
+    ok = encode_chunks(&tm_a, a.xq, a.M, a.K, kBlockM) && encode_chunks(&tm_b, a.wq, w_rows, a.K, kBRows) &&
+         encode_chunks(&tm_b_half, a.wq, w_rows, a.K, kBRows / 2);
   } else {
     ok = encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, a.M, a.K, kBlockM, kBlockK) &&
-         encode_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, a.N, a.K, kBRows, kBlockK) &&
-         encode_2d(&tm_b_half, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, a.N, a.K, kBRows / 2, kBlockK);
+         encode_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, w_rows, a.K, kBRows, kBlockK) &&
+         encode_2d(&tm_b_half, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, w_rows, a.K, kBRows / 2, kBlockK);
   }
   if constexpr (OUT == GemmOut::kBf16Dequant) {
     ok = ok && encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.M, a.N, 32, 64);
+  } else if constexpr (kGlu) {
+    ok = ok && encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.M, a.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   } else {
     ok = ok && encode_2d(&tm_d, EL == GemmElem::kE4M3 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_INT32,
                          4, a.out, a.M, a.N, 32, 32);
@@ -745,7 +877,7 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   p.N = static_cast<int>(a.N);
   p.K = static_cast<int>(a.K);
   p.m_tiles = static_cast<int>((a.M + kTileM - 1) / kTileM);
-  p.n_tiles = static_cast<int>((a.N + BN - 1) / BN);
+  p.n_tiles = static_cast<int>(kGlu ? (a.N + BN / 2 - 1) / (BN / 2) : (a.N + BN - 1) / BN);
   p.k_blocks = static_cast<int>((a.K + KCH * kBlockK - 1) / (KCH * kBlockK));
   p.num_tiles = p.m_tiles * p.n_tiles;
   p.full_tiles = p.num_tiles;
@@ -757,6 +889,7 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   p.bias = static_cast<const __nv_bfloat16*>(a.bias);
   p.timeout_ns = a.timeout_ns;
   p.err = nullptr;
+  p.gelu = a.act == W8A8_ACT_GELU;
   p.a_evict_first = a.M * a.K > a.l2_bytes / 2 ? 1 : 0;
   p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.ldx = a.ldx;
@@ -775,9 +908,10 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   if (units < 1) units = 1;
   if (units > p.num_tiles) units = p.num_tiles;
   // Last round: if at most half the CTAs (pairs) would get a tile, give each
-  // of the remaining tiles to two CTAs (pairs) as half-width items instead.
+  // of the remaining tiles to two CTAs (pairs) as half-width items instead
+  // (not the gated layer's on single CTAs, whose boxes are half-height already).
   const int tail = p.num_tiles % units;
-  if (BN == 256 && tail > 0 && 2 * tail <= units) {
+  if (BN == 256 && (PAIR || !kGlu) && tail > 0 && 2 * tail <= units) {
     p.full_tiles = p.num_tiles - tail;
     p.work_items = p.full_tiles + 2 * tail;
   }
@@ -837,40 +971,32 @@ int gemm_max_stages(int block_m, int block_n) {
   return s;
 }
 
+// The three outputs of one tile shape and operand format.
+template <int BN, bool PAIR, GemmElem EL, int KCH>
+cudaError_t launch_out(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t stream) {
+  switch (a.out_kind) {
+    case GemmOut::kBf16Dequant: return launch_typed<BN, GemmOut::kBf16Dequant, PAIR, false, EL, KCH>(a, cfg, stream);
+    case GemmOut::kGlu: return launch_typed<BN, GemmOut::kGlu, PAIR, false, EL, KCH>(a, cfg, stream);
+    default: return launch_typed<BN, GemmOut::kAcc32, PAIR, false, EL, KCH>(a, cfg, stream);
+  }
+}
+
 // Non-fused launches of one operand format.
 template <GemmElem EL>
 cudaError_t launch_plain(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t stream) {
-  using O = GemmOut;
-  const bool bf16 = a.out_kind == O::kBf16Dequant;
   if (cfg.block_m == 256) {
     // CTA pairs load two K-chunks per box when K allows it and the ring
     // holds at least two such stages.
     const bool chunks2 = a.K % 128 == 0 && cfg.stages >= 4;
     if (cfg.block_n == 256) {
-      if (chunks2) {
-        return bf16 ? launch_typed<256, O::kBf16Dequant, true, false, EL, 2>(a, cfg, stream)
-                    : launch_typed<256, O::kAcc32, true, false, EL, 2>(a, cfg, stream);
-      }
-      return bf16 ? launch_typed<256, O::kBf16Dequant, true, false, EL>(a, cfg, stream)
-                  : launch_typed<256, O::kAcc32, true, false, EL>(a, cfg, stream);
+      return chunks2 ? launch_out<256, true, EL, 2>(a, cfg, stream) : launch_out<256, true, EL, 1>(a, cfg, stream);
     }
     if (cfg.block_n == 128) {
-      if (chunks2) {
-        return bf16 ? launch_typed<128, O::kBf16Dequant, true, false, EL, 2>(a, cfg, stream)
-                    : launch_typed<128, O::kAcc32, true, false, EL, 2>(a, cfg, stream);
-      }
-      return bf16 ? launch_typed<128, O::kBf16Dequant, true, false, EL>(a, cfg, stream)
-                  : launch_typed<128, O::kAcc32, true, false, EL>(a, cfg, stream);
+      return chunks2 ? launch_out<128, true, EL, 2>(a, cfg, stream) : launch_out<128, true, EL, 1>(a, cfg, stream);
     }
   } else if (cfg.block_m == 128) {
-    if (cfg.block_n == 256) {
-      return bf16 ? launch_typed<256, O::kBf16Dequant, false, false, EL>(a, cfg, stream)
-                  : launch_typed<256, O::kAcc32, false, false, EL>(a, cfg, stream);
-    }
-    if (cfg.block_n == 128) {
-      return bf16 ? launch_typed<128, O::kBf16Dequant, false, false, EL>(a, cfg, stream)
-                  : launch_typed<128, O::kAcc32, false, false, EL>(a, cfg, stream);
-    }
+    if (cfg.block_n == 256) return launch_out<256, false, EL, 1>(a, cfg, stream);
+    if (cfg.block_n == 128) return launch_out<128, false, EL, 1>(a, cfg, stream);
   }
   return cudaErrorInvalidValue;
 }

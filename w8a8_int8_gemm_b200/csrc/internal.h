@@ -19,8 +19,10 @@ struct GemmConfig {
 };
 
 // kAcc32: the raw 32-bit accumulators (int32 for int8 operands, fp32 for
-// E4M3 operands) instead of the dequantized bf16 output.
-enum class GemmOut { kBf16Dequant = 0, kAcc32 = 1 };
+// E4M3 operands) instead of the dequantized bf16 output.  kGlu: wq holds two
+// projections (rows [0, N) the gate, [N, 2N) the other) and the output is
+// act(gate) * other in bf16.
+enum class GemmOut { kBf16Dequant = 0, kAcc32 = 1, kGlu = 2 };
 
 // Operand format: int8 (tcgen05 kind::i8, int32 accumulators) or OCP E4M3
 // (kind::f8f6f4, fp32 accumulators).
@@ -36,6 +38,7 @@ struct GemmArgs {
   int64_t M, N, K;
   GemmOut out_kind;
   GemmElem elem = GemmElem::kInt8;
+  int act = 0;  // kGlu: W8A8_ACT_SILU or W8A8_ACT_GELU
   uint64_t timeout_ns;
   int64_t l2_bytes = 0;  // L2 size of the device (chooses the A operand's cache policy)
   // The fused linear layer: quantize x [M, K] (bf16, row stride ldx) into
@@ -88,6 +91,9 @@ cudaError_t launch_selftest_wait(uint64_t timeout_ns, cudaStream_t stream);
 w8a8_status check_linear_io(const void* x, const int8_t* wq, const float* scale_w, const void* bias,
                             const void* out, int64_t M, int64_t N, int64_t K);
 w8a8_status check_current_device();
+// The same for the gated layer w8a8_linear_glu, its activation included.
+w8a8_status check_glu_call(const void* x, const int8_t* wq, const float* scale_w, const void* bias, const void* out,
+                           const void* ws_xq, const float* ws_scale_a, int64_t M, int64_t N, int64_t K, int32_t act);
 // check_linear_io plus the non-null, 16-byte aligned workspaces ws_xq and ws_scale_a.
 w8a8_status check_linear_call(const void* x, const int8_t* wq, const float* scale_w, const void* bias,
                               const void* out, const void* ws_xq, const float* ws_scale_a, int64_t M, int64_t N,
