@@ -424,6 +424,67 @@ typedef struct {
 W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t stream);
 
 /*
+ * Attention over packed documents (between a block's QKV and attention-output
+ * layers; over a key/value cache for single tokens).  Queries and keys are two
+ * streams of tokens cut into the same number of documents (a batch, packed
+ * images or prompts, sequences and their caches); a query sees keys of its own
+ * document only.  For query i and key j of a document with Lq queries and Lk
+ * keys, head h and its key/value head h / (heads_q / heads_k):
+ *   s = scale * sum_x q[i,h,x] * k[j,h',x]
+ *   s = cap * tanh(s / cap)                        if cap > 0
+ *   s = s - slopes[h] * |i + Lk - Lq - j|          if slopes is given
+ *   seen = !causal or j <= i + Lk - Lq or j < prefix[document]
+ *   out[i,h,:] = sum_j softmax_j(s)[j] * v[j,h',:]  over the keys seen
+ *   lse[i,h] = log sum_j exp(s[j])                  over the keys seen
+ * (the last query stands at the last key, as in a cache; a prefix longer than
+ * the document is the whole document).  A query that sees no key gets 0 and an
+ * lse of -inf.  Scores, maxima, sums and weighted sums are binary32; the
+ * weights exp(s - max) enter the product with v in bf16 (in two bf16 parts
+ * where queries are few); out is rounded once.
+ *
+ *   q, out   bf16 [tokens_q, heads_q, head_dim];  k, v  bf16 [tokens_k, heads_k,
+ *            head_dim]: the last dimension contiguous, ld* the stride of a
+ *            token and hs* of a head in elements (multiples of 8, at least
+ *            head_dim where there is more than one): views of a QKV buffer or
+ *            head-major tensors.  out's rows may not overlap one another, nor
+ *            any other argument.
+ *   lse      fp32 [tokens_q, heads_q] contiguous, or NULL
+ *   cu_q, cu_k  int32 [docs + 1] on the device, not decreasing: document d has
+ *            the tokens cu[d] .. cu[d+1]-1.  NULL: docs equal parts (the number
+ *            of tokens is then a multiple of docs).  Documents may be empty;
+ *            tokens before cu[0] and from cu[docs] on belong to none, and their
+ *            rows of out and lse are left as they were.  Values are clamped to
+ *            [0, tokens]; decreasing ones give unspecified rows of out.
+ *   prefix   int32 [docs] on the device or NULL; only with causal
+ *   slopes   fp32 [heads_q] on the device or NULL
+ * Keys, values and queries outside a document, whatever they hold, do not
+ * change its results; neither do keys a mask hides.  A value row v[j] that is
+ * hidden from one query but seen by another of its document must be finite.
+ * head_dim 64 or 128; heads_q a multiple of heads_k, up to 65536; docs >= 1;
+ * tokens up to 2^30; scale > 0; 0 <= cap <= 1e6 (0: no cap; a cap adds an
+ * error of 1e-6 * cap to a score).  tokens_q == 0 launches nothing.
+ */
+typedef struct {
+    const void* q;
+    const void* k;
+    const void* v;
+    void* out;
+    float* lse;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    const int32_t* prefix;
+    const float* slopes;
+    int64_t tokens_q, tokens_k;
+    int64_t ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso;
+    int32_t docs, heads_q, heads_k, head_dim;
+    int32_t causal;           /* 0 or 1 */
+    float scale;
+    float cap;
+} w8a8_attention_desc;
+
+W8A8_API w8a8_status w8a8_attention(const w8a8_attention_desc* desc, w8a8_stream_t stream);
+
+/*
  * A chain of W8A8 linear layers as one CUDA graph (the paper drops its
  * kernel into every linear layer of the DiT, abstract; a DiT block runs
  * four: attention QKV, attention output, MLP up, MLP down).  Each layer is

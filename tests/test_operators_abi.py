@@ -78,3 +78,32 @@ def test_chain_with_gated_layers(w8):
         assert w8.raw_lib().w8a8_chain_create(d, 1, ctypes.byref(h)) == 1 and not h.value
     d = (w8.LinearDesc * 1)(w8.LinearDesc(A, A, A, None, A, A + 4, A, 4, 8, 32, 0, 2))
     assert w8.raw_lib().w8a8_chain_create(d, 1, ctypes.byref(h)) == 2 and not h.value
+
+
+def attention(w8, **change):
+    d = w8.AttentionDesc(q=A, k=A, v=A, out=A, lse=A, cu_q=A, cu_k=A, prefix=None, slopes=None, tokens_q=4,
+                         tokens_k=8, ldq=128, hsq=64, ldk=64, hsk=64, ldv=64, hsv=64, ldo=128, hso=64, docs=2,
+                         heads_q=2, heads_k=1, head_dim=64, causal=0, scale=0.125, cap=0.0)
+    for name, value in change.items():
+        setattr(d, name, value)
+    return w8.raw_lib().w8a8_attention(ctypes.byref(d), None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(tokens_q=-1), 1), (dict(tokens_k=-1), 1), (dict(tokens_q=2 ** 30 + 1), 1), (dict(docs=0), 1),
+    (dict(docs=2 ** 24 + 1), 1), (dict(heads_k=0), 1), (dict(heads_q=1, heads_k=2), 1), (dict(heads_q=3, heads_k=2), 1),
+    (dict(heads_q=65537), 1), (dict(head_dim=96), 1), (dict(head_dim=256), 1), (dict(cu_q=None, tokens_q=5), 1),
+    (dict(cu_k=None, tokens_k=7), 1), (dict(causal=2), 1), (dict(prefix=A), 1), (dict(scale=0.0), 1),
+    (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(cap=-1.0), 1),
+    (dict(cap=float("nan")), 1), (dict(cap=2e6), 1), (dict(q=None), 1), (dict(v=None), 1), (dict(out=None), 1),
+    (dict(ldq=32), 1), (dict(ldk=0), 1), (dict(hsq=0), 1), (dict(ldo=64), 1), (dict(hso=8), 1), (dict(ldv=2 ** 31), 1),
+    (dict(ldk=-64), 1), (dict(k=A + 8), 2), (dict(out=A + 2), 2), (dict(ldv=68), 2), (dict(hsq=68, ldq=136), 2),
+    (dict(cu_q=A + 2), 2), (dict(lse=A + 1), 2), (dict(slopes=A + 2), 2),
+    (dict(tokens_q=0), 0), (dict(tokens_q=0, q=None, out=None), 0),
+])
+def test_attention(w8, change, status):
+    assert attention(w8, **change) == status
+
+
+def test_attention_needs_arguments(w8):
+    assert w8.raw_lib().w8a8_attention(None, None) == 1

@@ -33,7 +33,7 @@ __all__ = [
     "w8a8_quantize_act_gelu", "w8a8_gelu", "w8a8_linear_gelu", "ACT_NONE", "ACT_GELU", "ACT_SILU",
     "w8a8_gemm_glu", "w8a8_gemm_glu_ex", "w8a8_gemm_glu_fp8", "w8a8_gemm_glu_fp8_ex", "w8a8_linear_glu",
     "w8a8_linear_glu_fp8",
-    "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS",
+    "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS", "w8a8_attention",
     "LinearDesc", "Chain", "linear_layer", "w8a8_chain_create", "w8a8_chain_launch", "w8a8_chain_layers",
     "w8a8_chain_destroy",
     "w8a8_select_config",
@@ -86,6 +86,15 @@ class QkDesc(ctypes.Structure):
                 + [("eps", ctypes.c_float)])
 
 
+class AttentionDesc(ctypes.Structure):
+    """w8a8_attention_desc: the arguments of w8a8_attention."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "cu_q", "cu_k", "prefix", "slopes")]
+                + [(n, ctypes.c_int64) for n in ("tokens_q", "tokens_k", "ldq", "hsq", "ldk", "hsk", "ldv", "hsv",
+                                                 "ldo", "hso")]
+                + [(n, ctypes.c_int32) for n in ("docs", "heads_q", "heads_k", "head_dim", "causal")]
+                + [("scale", ctypes.c_float), ("cap", ctypes.c_float)])
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(lib_path):
         raise ImportError(
@@ -124,6 +133,7 @@ def _load() -> ctypes.CDLL:
         "w8a8_linear_glu": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
         "w8a8_linear_glu_fp8": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
         "w8a8_qk_norm_rope": ([ctypes.POINTER(QkDesc), p], ctypes.c_int),
+        "w8a8_attention": ([ctypes.POINTER(AttentionDesc), p], ctypes.c_int),
         "w8a8_chain_create": ([ctypes.POINTER(LinearDesc), i32, ctypes.POINTER(p)], ctypes.c_int),
         "w8a8_chain_launch": ([p, p], ctypes.c_int),
         "w8a8_chain_layers": ([p], i32),
@@ -722,6 +732,48 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     with torch.cuda.device(dev):
         _check(_lib.w8a8_qk_norm_rope(ctypes.byref(desc), _stream(stream, dev)), "w8a8_qk_norm_rope")
     return q_out, k_out
+
+
+def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal: bool = False, cu_q=None, cu_k=None,
+                   docs: int | None = None, prefix=None, slopes=None, out=None, lse=None, stream=None):
+    """Softmax attention over packed documents: out bf16 [Tq, Hq, D] from q [Tq, Hq, D] and k, v [Tk, Hk, D]
+    (Hq a multiple of Hk, D 64 or 128, strided views allowed).
+
+    cu_q, cu_k: int32 [docs + 1] starts of the documents in each stream; without them docs (default 1) equal
+    parts.  scale defaults to D ** -0.5; cap > 0 caps the scores by cap * tanh(s / cap); causal with prefix
+    (int32 [docs]) shows each query the keys up to its own place and the document's prefix; slopes (fp32 [Hq])
+    subtracts slope * distance.  lse: fp32 [Tq, Hq] tensor that receives the scores' log-sum-exp.  See
+    include/w8a8.h."""
+    ldq, hsq = _heads(q, "q")
+    Tq, Hq, D = q.shape
+    ldk, hsk = _heads(k, "k", D)
+    ldv, hsv = _heads(v, "v", D)
+    Tk, Hk = k.shape[:2]
+    if tuple(v.shape) != tuple(k.shape):
+        raise ValueError(f"v must have the shape of k, got {tuple(v.shape)} and {tuple(k.shape)}")
+    for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        if c is not None:
+            _need(c, name, torch.int32, 1)
+            docs = c.shape[0] - 1 if docs is None else docs
+    docs = 1 if docs is None else int(docs)
+    for c, name, n, kind in ((cu_q, "cu_q", docs + 1, torch.int32), (cu_k, "cu_k", docs + 1, torch.int32),
+                             (prefix, "prefix", docs, torch.int32), (slopes, "slopes", Hq, torch.float32)):
+        if c is not None:
+            _need_contig(c, name, kind, (n,))
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
+    ldo, hso = _heads(out, "out", D)
+    if out.shape != q.shape:
+        raise ValueError(f"out must have the shape of q, got {tuple(out.shape)}")
+    if lse is not None:
+        _need_contig(lse, "lse", torch.float32, (Tq, Hq))
+    dev = _one_device(q, k, v, cu_q, cu_k, prefix, slopes, out, lse)
+    desc = AttentionDesc(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_q), _ptr(cu_k), _ptr(prefix),
+                         _ptr(slopes), Tq, Tk, ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D,
+                         1 if causal else 0, float(D ** -0.5 if scale is None else scale), float(cap))
+    with torch.cuda.device(dev):
+        _check(_lib.w8a8_attention(ctypes.byref(desc), _stream(stream, dev)), "w8a8_attention")
+    return out
 
 
 # ------------------------------------------------- chains of linear layers

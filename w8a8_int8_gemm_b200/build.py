@@ -21,8 +21,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libw8a8.so")
 
-SOURCES = ["api.cu", "quant.cu", "gemm_sm100.cu", "linear_noalloc.cu", "chain.cu", "qk_norm_rope.cu"]
-HEADERS = ["internal.h", "sm100_ptx.cuh", "quant_row.cuh"]
+SOURCES = ["api.cu", "quant.cu", "gemm_sm100.cu", "linear_noalloc.cu", "chain.cu", "qk_norm_rope.cu", "attention.cu",
+           "attention_rows.cu"]
+HEADERS = ["internal.h", "sm100_ptx.cuh", "quant_row.cuh", "attention.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

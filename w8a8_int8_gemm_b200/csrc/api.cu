@@ -226,11 +226,15 @@ w8a8_status check_glu_call(const void* x, const int8_t* wq, const float* scale_w
 }
 
 // W8A8_OK if the current device is supported (sm_100), from the cached
-// device properties.
-w8a8_status check_current_device() {
+// device properties; *sms, if asked for, its number of SMs.
+w8a8_status check_current_device(int* sms) {
   DeviceInfo dev;
-  return current_device(&dev);
+  const w8a8_status st = current_device(&dev);
+  if (st == W8A8_OK && sms != nullptr) *sms = dev.sms;
+  return st;
 }
+
+uint64_t wait_timeout_ns() { return static_cast<uint64_t>(g_timeout_ns.load()); }
 
 }  // namespace w8a8
 

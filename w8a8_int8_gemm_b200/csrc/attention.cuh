@@ -1,0 +1,109 @@
+// attention.cuh -- what the two attention kernels share: their arguments, the
+// packed documents, the masks as one limit per query, and the scores.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace w8a8 {
+
+struct AttnParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* out;
+  float* lse;  // [tokens_q, heads_q] or null
+  const int32_t* cu_q;
+  const int32_t* cu_k;  // document starts, or null: documents of equal length
+  const int32_t* prefix;
+  const float* slopes;
+  int64_t ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso;
+  int tokens_q, tokens_k, docs;
+  int heads_q, heads_k, group;  // group = heads_q / heads_k
+  bool causal;
+  float scale, cap;
+  uint64_t timeout_ns;
+};
+
+cudaError_t launch_attention_rows(const AttnParams& p, int head_dim, int sms, cudaStream_t stream);
+cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, cudaStream_t stream);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+#ifdef __CUDACC__
+
+// One document: its tokens in the packed streams and its masks.
+struct Doc {
+  int q0, lq, k0, lk;
+  int shift;   // query i stands at key place i + shift (the last query at the last key)
+  int prefix;  // keys every query sees
+};
+
+// Start of document d in a stream of `tokens` tokens; whatever cu holds, the
+// result is in [0, tokens], so no index built from it leaves the stream.
+__device__ __forceinline__ int doc_start(const int32_t* cu, int d, int docs, int tokens) {
+  if (cu == nullptr) return d * (tokens / docs);
+  return min(max(__ldg(cu + d), 0), tokens);
+}
+
+// Work slots of `rows` rows (query tokens times `per` rows each) are numbered
+// over the documents without a table: document d's slots begin at
+// floor(start_d * per / rows) + d, which leaves room for every document's
+// slots (a document of n rows needs at most floor((s + n)/rows) - floor(s/rows)
+// + 1 of them) and at most one unused slot per document.  slot_doc finds the
+// last document that begins at or before a slot, 32 candidates at a time (one
+// load for up to 32 documents); all lanes of the warp return the same.
+__device__ __forceinline__ int slot_begin(const AttnParams& p, int d, int per, int rows) {
+  return static_cast<int>(static_cast<int64_t>(doc_start(p.cu_q, d, p.docs, p.tokens_q)) * per / rows) + d;
+}
+
+__device__ __forceinline__ int slot_doc(const AttnParams& p, int slot, int per, int rows) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.docs;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int d = lo + lane * step;
+    const bool before = d < lo + n && slot_begin(p, d, per, rows) <= slot;
+    const int count = max(1, __popc(__ballot_sync(0xFFFFFFFFu, before)));
+    const int skip = (count - 1) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ Doc load_doc(const AttnParams& p, int d) {
+  Doc r;
+  r.q0 = doc_start(p.cu_q, d, p.docs, p.tokens_q);
+  r.lq = max(0, doc_start(p.cu_q, d + 1, p.docs, p.tokens_q) - r.q0);
+  r.k0 = doc_start(p.cu_k, d, p.docs, p.tokens_k);
+  r.lk = max(0, doc_start(p.cu_k, d + 1, p.docs, p.tokens_k) - r.k0);
+  r.shift = r.lk - r.lq;
+  r.prefix = p.prefix != nullptr ? min(max(__ldg(p.prefix + d), 0), r.lk) : 0;
+  return r;
+}
+
+// Every mask here leaves query i the keys j < limit: all of the document's, or
+// those up to its own place and the prefix.
+__device__ __forceinline__ int key_limit(const AttnParams& p, const Doc& d, int i) {
+  return p.causal ? min(max(i + d.shift + 1, d.prefix), d.lk) : d.lk;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap * log2(e) * tanh(s * scale / cap), from tanh(y) = 1 - 2 / (1 + exp(2y)):
+// within 3e-7 of tanh, so within 5e-7 * cap of the score.
+__device__ __forceinline__ float capped(float s, float two_log2e_scale_over_cap, float cap_log2e) {
+  return cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(s * two_log2e_scale_over_cap));
+}
+
+#endif  // __CUDACC__
+
+}  // namespace w8a8

@@ -90,7 +90,8 @@ cudaError_t launch_selftest_wait(uint64_t timeout_ns, cudaStream_t stream);
 // workspaces), made before any CUDA call; and the current device's support.
 w8a8_status check_linear_io(const void* x, const int8_t* wq, const float* scale_w, const void* bias,
                             const void* out, int64_t M, int64_t N, int64_t K);
-w8a8_status check_current_device();
+w8a8_status check_current_device(int* sms = nullptr);
+uint64_t wait_timeout_ns();  // the limit of every bounded wait (w8a8_set_wait_timeout_ns)
 // The same for the gated layer w8a8_linear_glu, its activation included.
 w8a8_status check_glu_call(const void* x, const int8_t* wq, const float* scale_w, const void* bias, const void* out,
                            const void* ws_xq, const float* ws_scale_a, int64_t M, int64_t N, int64_t K, int32_t act);
