@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libw8a8.so")
 
 SOURCES = ["api.cu", "quant.cu", "gemm_sm100.cu", "linear_noalloc.cu", "chain.cu", "qk_norm_rope.cu", "attention.cu",
-           "attention_rows.cu"]
+           "attention_rows.cu", "attention_sm100.cu"]
 HEADERS = ["internal.h", "sm100_ptx.cuh", "quant_row.cuh", "attention.cuh"]
 
 NVCC_FLAGS = [

@@ -92,5 +92,9 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
   p.cap = a->cap;
   p.timeout_ns = wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return status_of(launch_attention_rows(p, a->head_dim, sms, s));
+  // Queries of a document (on average) times the heads that share keys: up to 64 rows, reading K and V bounds
+  // the call, and the row kernel reads them once for 16 rows (from L2 for the next ones).
+  const int64_t rows = a->tokens_q * p.group;
+  if (rows <= int64_t{64} * a->docs) return status_of(launch_attention_rows(p, a->head_dim, sms, s));
+  return status_of(launch_attention_tiles(p, a->head_dim, s));
 }

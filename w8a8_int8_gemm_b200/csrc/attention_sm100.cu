@@ -1,0 +1,518 @@
+// attention_sm100.cu -- attention for many queries, on the 5th-generation
+// tensor cores.
+//
+// A CTA takes 256 queries of one document and head, as two sub-tiles of 128
+// (the rows of a tcgen05.mma), and walks the keys 128 at a time:
+//   S = Q K^T       Q and K from shared memory, S in tensor memory
+//   P = 2^(S c - m) rounded to bf16, written over S in tensor memory
+//   O += P V        P from tensor memory, V from shared memory
+// with the running maximum m and sum of a softmax per query.  O stays in
+// tensor memory: it is rescaled only when a row's maximum has grown by more
+// than 2^8 since m was last set (P then reaches 2^8 at most, and the sum is
+// binary32), so in most tiles no thread touches it.
+//
+//   warps 0-3, 4-7  softmax of sub-tile 0 / 1; a thread owns a query, so
+//                   maximum and sum need no exchange
+//   warp 8          loads Q, then K and V tiles through a ring (TMA)
+//   warp 9          issues the MMAs: while one sub-tile's softmax runs, the
+//                   tensor cores work for the other; it also zeroes the
+//                   rows of the last V tile that lie behind the document's
+//                   end (a weight of 0 times whatever is there must be 0)
+//
+// The tensor cores execute MMAs in the order they are issued, so S of tile
+// j + 1 may overwrite P of tile j right behind O += P V, and "S full" also
+// says that O holds every tile before.
+//
+// What bounds it: a 128 x 128 tile costs 4 D * 128 * 128 operations of the
+// tensor cores (1024 cycles at D = 128, 512 at D = 64) and 128 * 128
+// exponentials of the special-function units (1024 cycles).
+#include <cuda.h>
+
+#include <cstring>
+
+#include "attention.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kSub = 128;             // queries of a sub-tile
+constexpr int kTileQ = 2 * kSub;      // queries of a CTA
+constexpr int kTileK = 128;           // keys of a tile
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208;     // 256 * 208 + 128 * 88 = 384 * 168, the registers the CTA starts with
+constexpr int kRegsOther = 88;
+constexpr int kBlockBytes = 128 * 128;  // 128 rows x 64 values
+constexpr int kBarrierBytes = 256;
+constexpr float kGrowth = 8.0f;       // log2 of the growth of a row's maximum that rescales O
+
+__host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBlockBytes; }
+__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 5 : 8; }
+__host__ __device__ constexpr int smem_bytes(int D) {
+  return 1024 + (2 + ring_stages(D)) * tile_bytes(D) + kBarrierBytes;
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int D, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const AttnParams p, const int slots, int* err) {
+  constexpr int kStages = ring_stages(D);
+  constexpr int kTile = tile_bytes(D);
+  constexpr int kBlocks = D / 64;
+  constexpr uint32_t kIdescS = make_idesc_bf16(kSub, kTileK, false);
+  constexpr uint32_t kIdescO = make_idesc_bf16(kSub, D, true);
+  constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 columns each), O0, O1 (D each)
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* ring = sQ + 2 * kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * kTile);
+  uint64_t* empty = full + kStages;
+  uint64_t* q_full = empty + kStages;   // [2]
+  uint64_t* s_full = q_full + 2;        // [2]
+  uint64_t* p_full = s_full + 2;        // [2]
+  uint64_t* o_full = p_full + 2;        // [2]
+  uint64_t* drain = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // Causal documents: the slots with the most keys first, so that the last CTAs to start are short ones.
+  // Otherwise a head's slots side by side, which share its keys and values.
+  const int block = static_cast<int>(blockIdx.x);
+  const int head = p.causal ? block % p.heads_q : block / slots;
+  const int slot = p.causal ? slots - 1 - block / p.heads_q : block % slots;
+  const int d = slot_doc(p, slot, 1, kTileQ);
+  const Doc doc = load_doc(p, d);
+  const int row0 = (slot - slot_begin(p, d, 1, kTileQ)) * kTileQ;
+  const int rows = min(kTileQ, doc.lq - row0);
+  if (rows <= 0 || row0 < 0) return;  // an unused slot
+  const int kv_head = head / p.group;
+  // Key tiles of each sub-tile (limits grow with the query).
+  auto key_tiles = [&](int s) {
+    const int n = min(kSub, rows - s * kSub);
+    return n <= 0 ? 0 : (max(0, key_limit(p, doc, row0 + s * kSub + n - 1)) + kTileK - 1) / kTileK;
+  };
+  const int n0 = key_tiles(0), n1 = key_tiles(1);
+  const int tiles = max(n0, n1);
+  const int tail_rows = doc.lk - (tiles - 1) * kTileK;  // rows of the last V tile that are the document's
+  const bool tail = tiles > 0 && tail_rows < kTileK;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&o_full[s], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish_alloc_permit();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= 8) {
+    reg_lower<kRegsOther>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ loader
+      const uint64_t keep = l2_policy_evict_last();
+      const uint64_t once = l2_policy_evict_first();
+      int fills = 0;
+      int q_loads = 0;
+      bool ok = true;
+      auto load_q = [&](int s) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[s], kTile);
+          for (int b = 0; b < kBlocks; ++b) {
+            tma_load_3d_hint(sQ + s * kTile + b * kBlockBytes, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub,
+                             head, once);
+          }
+        }
+        __syncwarp();
+        ++q_loads;
+      };
+      if (n0 > 0) load_q(0);
+      for (int f = 0; f < 2 * tiles; ++f) {
+        const int stage = f % kStages;
+        ok = warp_wait(&empty[stage], static_cast<uint32_t>((f / kStages) & 1) ^ 1u, abort_flag, p.timeout_ns, err,
+                       kSiteAttnLoad);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[stage], kTile);
+          for (int b = 0; b < kBlocks; ++b) {
+            tma_load_3d_hint(ring + stage * kTile + b * kBlockBytes, (f & 1) ? &tm_v : &tm_k, &full[stage], 64 * b,
+                             doc.k0 + (f >> 1) * kTileK, kv_head, keep);
+          }
+        }
+        __syncwarp();
+        ++fills;
+        if (f == 0 && n1 > 0) load_q(1);
+      }
+      // Every load must have landed before the CTA ends (on the normal path they have).
+      if (lane == 0) {
+        for (int f = max(0, fills - kStages); f < fills; ++f) {
+          mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
+        }
+        if (n0 > 0) mbar_wait_drain(&q_full[0], 0, p.timeout_ns, err);
+        if (q_loads > (n0 > 0 ? 1 : 0)) mbar_wait_drain(&q_full[1], 0, p.timeout_ns, err);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // -------------------------------------------------------- MMA issuer
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        if (ok) ok = warp_wait(bar, parity, abort_flag, p.timeout_ns, err, site);
+      };
+      auto wait_fill = [&](int f) { wait(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), kSiteAttnOperand); };
+      auto scores = [&](int s, int j) {  // S_s = Q_s K_j^T
+        wait_fill(2 * j);
+        if (!ok) return;
+        tc_fence_after_sync();
+        if (lane == 0) {
+          const uint32_t q = smem_u32(sQ + s * kTile);
+          const uint32_t k = smem_u32(ring + (2 * j % kStages) * kTile);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = (x / 4) * kBlockBytes;
+            mma_bf16_ss(tmem + s * kTileK, make_smem_desc_k_sw128(q + off) + 2 * (x % 4),
+                        make_smem_desc_k_sw128(k + off) + 2 * (x % 4), kIdescS, x > 0);
+          }
+          mma_commit(&s_full[s]);
+        }
+        __syncwarp();
+      };
+      if (n0 > 0) {
+        wait(&q_full[0], 0, kSiteAttnOperand);
+        scores(0, 0);
+      }
+      if (n1 > 0) {
+        wait(&q_full[1], 0, kSiteAttnOperand);
+        scores(1, 0);
+      }
+      if (ok && tiles > 0 && lane == 0) mma_commit(&empty[0]);
+      __syncwarp();
+      for (int j = 0; ok && j < tiles; ++j) {
+        const int vf = 2 * j + 1;
+        wait_fill(vf);
+        if (!ok) break;
+        if (tail && j == tiles - 1) {
+          uint8_t* v = ring + (vf % kStages) * kTile;
+          for (int x = tail_rows * 8 + lane; x < kTileK * 8; x += 32) {
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+              *reinterpret_cast<uint4*>(v + b * kBlockBytes + x * 16) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        for (int s = 0; s < 2; ++s) {
+          const int n = s == 0 ? n0 : n1;
+          if (j >= n) continue;
+          wait(&p_full[s], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (lane == 0) {
+            const uint32_t v = smem_u32(ring + (vf % kStages) * kTile);
+#pragma unroll
+            for (int x = 0; x < kTileK / 16; ++x) {
+              mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x,
+                          make_smem_desc_n_sw128(v + x * 16 * 128, kBlockBytes), kIdescO, (j > 0 || x > 0) ? 1u : 0u);
+            }
+            if (j + 1 == n) mma_commit(&o_full[s]);
+          }
+          __syncwarp();
+          if (j + 1 < n) scores(s, j + 1);
+          if (!ok) break;
+        }
+        if (ok && lane == 0) {
+          mma_commit(&empty[vf % kStages]);
+          if (j + 1 < tiles) mma_commit(&empty[(vf + 1) % kStages]);
+        }
+        __syncwarp();
+      }
+      // No MMA may still run when tensor memory is freed.
+      if (lane == 0) {
+        mma_commit(drain);
+        mbar_wait_drain(drain, 0, p.timeout_ns, err);
+      }
+      __syncwarp();
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    reg_raise<kRegsSoftmax>();
+    const int s = warp >> 2;
+    const int quarter = warp & 3;
+    const int my_rows = min(kSub, rows - s * kSub);  // <= 0: nothing in this sub-tile
+    const int n = s == 0 ? n0 : n1;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lanes + s * kTileK;
+    const uint32_t t_o = tmem + lanes + 2 * kTileK + s * D;
+    const int in_sub = quarter * 32 + lane;
+    const int i = row0 + s * kSub + in_sub;  // the thread's query
+    const int limit = in_sub < my_rows ? max(0, key_limit(p, doc, i)) : 0;
+    const int least = my_rows > 0 ? key_limit(p, doc, row0 + s * kSub) : 0;  // the sub-tile's smallest limit
+    constexpr bool kChange = CAP || BIAS;  // scores need more than the factor c
+    const float c = p.scale * kLog2e;
+    const float c_tanh = CAP ? 2.0f * kLog2e * p.scale / p.cap : 0.0f;
+    const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
+    const float slope = BIAS ? __ldg(p.slopes + head) * kLog2e : 0.0f;
+    const float place = static_cast<float>(i + doc.shift);
+
+    float m = -INFINITY;  // in units of log2
+    float l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      ok = warp_wait(&s_full[s], static_cast<uint32_t>(j & 1), abort_flag, p.timeout_ns, err, kSiteAttnScores);
+      if (!ok) break;
+      tc_fence_after_sync();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_load_32cols_async(t_s + 32 * b, v[b]);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_wait_load(v[b]);
+
+      if constexpr (kChange) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            float y = __uint_as_float(v[b][x]);
+            y = CAP ? capped(y, c_tanh, c_cap) : y * c;
+            if (BIAS) y -= slope * fabsf(place - static_cast<float>(j * kTileK + 32 * b + x));
+            v[b][x] = __float_as_uint(y);
+          }
+        }
+      }
+      if ((j + 1) * kTileK > least) {
+        const int left = limit - j * kTileK;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            if (32 * b + x >= left) v[b][x] = 0xFF800000u;  // -inf
+          }
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1]));
+      }
+      if (!kChange) top *= c;  // c > 0
+      if (j == 0) {
+        m = top;
+      } else {
+        const bool grow = top > m + kGrowth;
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float f = grow ? ex2(m - top) : 1.0f;
+          if (grow) m = top;
+          l *= f;
+#pragma unroll
+          for (int b = 0; b < D / 32; ++b) {
+            uint32_t o[32];
+            tmem_load_32cols(t_o + 32 * b, o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_store_32cols(t_o + 32 * b, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      const uint64_t c2 = pair(kChange ? 1.0f : c, kChange ? 1.0f : c), minus = pair(-base, -base);
+      uint64_t sum = pair(0.0f, 0.0f);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint64_t y = pair(__uint_as_float(v[b][2 * x]), __uint_as_float(v[b][2 * x + 1]));
+          float a0, a1;
+          unpair(kChange ? add2(y, minus) : fma2(y, c2, minus), a0, a1);
+          a0 = ex2(a0);
+          a1 = ex2(a1);
+          sum = add2(sum, pair(a0, a1));
+          w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
+        }
+        tmem_store_16cols(t_s + 16 * b, w);
+      }
+      float s0, s1;
+      unpair(sum, s0, s1);
+      l += s0 + s1;
+      tmem_wait_store();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
+    }
+
+    // ------------------------------------------------------------- epilogue
+    if (ok && n > 0) ok = warp_wait(&o_full[s], 0, abort_flag, p.timeout_ns, err, kSiteAttnOut);
+    if (ok && my_rows > 0) {
+      tc_fence_after_sync();
+      const bool any = limit > 0;
+      const float inv = any ? 1.0f / l : 0.0f;
+      // The warp's 32 rows through shared memory (its part of the sub-tile's Q, which no MMA reads any more),
+      // so that a row leaves in whole 128-byte lines.
+      constexpr int kRowBytes = 2 * D;
+      constexpr int kVec = kRowBytes / 16;
+      uint8_t* stage = sQ + s * kTile + quarter * 32 * kRowBytes;
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_load_32cols(t_o + 32 * b, o);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float a0 = __uint_as_float(o[8 * x + 2 * y]) * inv, a1 = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
+            w[y] = any ? pack_bf16(a0, a1) : 0u;
+          }
+          *reinterpret_cast<uint4*>(stage + lane * kRowBytes + (((4 * b + x) ^ (lane & 7)) * 16)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();
+      const int64_t token0 = doc.q0 + row0 + s * kSub + quarter * 32;
+      const int valid = min(32, my_rows - quarter * 32);
+#pragma unroll 4
+      for (int e = lane; e < 32 * kVec; e += 32) {
+        const int r = e / kVec, x = e % kVec;
+        if (r < valid) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((x ^ (r & 7)) * 16));
+          *reinterpret_cast<uint4*>(p.out + (token0 + r) * p.ldo + head * p.hso + x * 8) = w;
+        }
+      }
+      if (p.lse != nullptr && in_sub < my_rows) {
+        p.lse[(token0 + lane) * p.heads_q + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  if (*abort_flag) {
+    // A wait ran out: give copies already issued time to land before the shared memory they target is released.
+    if (threadIdx.x == 0) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 200000ull) {
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 9) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// {64 values, tokens, heads} boxes of 64 x 128 x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
+bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),
+                              static_cast<cuuint64_t>(heads)};
+  // (the stride of a dimension of one is free)
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (tokens > 1 ? ld : D)),
+                                 static_cast<cuuint64_t>(2 * (heads > 1 ? hs : D))};
+  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool CAP, bool BIAS>
+cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
+  CUtensorMap tm_q, tm_k, tm_v;
+  std::memset(&tm_q, 0, sizeof tm_q);
+  // No keys: no tile of them is ever loaded, and the maps describe q.
+  const bool none = p.tokens_k == 0;
+  bool ok = encode_heads(&tm_q, p.q, D, p.tokens_q, p.heads_q, p.ldq, p.hsq);
+  tm_k = tm_v = tm_q;
+  if (!none) {
+    ok = ok && encode_heads(&tm_k, p.k, D, p.tokens_k, p.heads_k, p.ldk, p.hsk) &&
+         encode_heads(&tm_v, p.v, D, p.tokens_k, p.heads_k, p.ldv, p.hsv);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  int* err = nullptr;
+  cudaError_t e = error_word_address(&err);
+  if (e != cudaSuccess) return e;
+  auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
+  constexpr int smem = smem_bytes(D);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t slots = p.tokens_q / kTileQ + p.docs;
+  if (slots * p.heads_q > 2147483647) return cudaErrorInvalidValue;
+  kernel<<<static_cast<unsigned>(slots * p.heads_q), kThreads, smem, stream>>>(tm_q, tm_k, tm_v, p,
+                                                                              static_cast<int>(slots), err);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, cudaStream_t stream) {
+  const bool cap = p.cap > 0.0f, bias = p.slopes != nullptr;
+  if (head_dim == 64) {
+    if (cap) return bias ? launch<64, true, true>(p, stream) : launch<64, true, false>(p, stream);
+    return bias ? launch<64, false, true>(p, stream) : launch<64, false, false>(p, stream);
+  }
+  if (cap) return bias ? launch<128, true, true>(p, stream) : launch<128, true, false>(p, stream);
+  return bias ? launch<128, false, true>(p, stream) : launch<128, false, false>(p, stream);
+}
+
+}  // namespace w8a8

@@ -1,6 +1,7 @@
 // internal.h -- launchers shared between the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -75,6 +76,14 @@ cudaError_t launch_gelu(const void* h, int64_t M, int64_t K, int64_t ldh, void* 
 // Kernel setup for launch_quantize_act_gelu on rows of K, made before a
 // stream capture that will record it.
 cudaError_t prepare_quantize_act_gelu(int64_t K, cudaStream_t stream);
+
+// cuTensorMapEncodeTiled (null if the driver has none) and the current
+// device's error word.
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_fn();
+cudaError_t error_word_address(int** out);
 
 // Largest stage count the shared memory holds for a tile shape (0 if none).
 // block_m 128: one CTA per tile; block_m 256: a CTA pair (cluster of 2).

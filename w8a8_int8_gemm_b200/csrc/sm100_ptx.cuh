@@ -21,6 +21,11 @@ enum WaitSite : int {
   kSiteDrain = 5,           // teardown waiting for in-flight copies / MMAs
   kSiteSelfTest = 6,        // the timeout self-test
   kSiteRowsReady = 7,       // fused linear: waiting for a block of quantized rows
+  kSiteAttnLoad = 8,        // attention: loader waiting for a free ring slot
+  kSiteAttnOperand = 9,     // attention: MMA issuer waiting for Q, K or V
+  kSiteAttnWeights = 10,    // attention: MMA issuer waiting for a tile of weights
+  kSiteAttnScores = 11,     // attention: softmax waiting for a tile of scores
+  kSiteAttnOut = 12,        // attention: softmax waiting for the weighted sum
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -435,6 +440,73 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
       : "memory");
 }
 
+// --- bf16 operands (kind::f16, K = 16 per instruction, fp32 accumulators)
+
+// Instruction descriptor: D format 1 (f32) in [4,6), A and B formats 1 (bf16)
+// in [7,10) and [10,13), B stored with N (not K) contiguous in bit 16, N >> 3
+// in [17,23), M >> 4 in [24,29).
+__host__ __device__ constexpr uint32_t make_idesc_bf16(int M, int N, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(b_n_major) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor of an operand stored with N contiguous, as
+// TMA lands [k rows][64 n] boxes with the 128-byte swizzle: 8 rows of k are
+// 1024 bytes (the stride-dimension offset), the next 64 columns of n
+// block_bytes further on (the leading-dimension offset).
+__device__ __forceinline__ uint64_t make_smem_desc_n_sw128(uint32_t smem_addr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over one K = 16 slice.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with A in tensor memory: 16 values of a row in 8 columns, the
+// lower one of a pair in the low half.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 3-D tile load into this CTA's shared memory with an L2 eviction-priority policy.
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* map, uint64_t* bar, int32_t x, int32_t y,
+                                                 int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+// Registers per thread of this warpgroup (a multiple of 8; all its warps execute it).
+template <int N>
+__device__ __forceinline__ void reg_raise() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_lower() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 values to two OCP E4M3 codes, each rounded to nearest (ties to
 // even) and saturated to +-448: `lo` in bits [0,8), `hi` in bits [8,16).
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
@@ -478,6 +550,19 @@ __device__ __forceinline__ void tmem_load_32cols_async(uint32_t taddr, uint32_t 
 __device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : W8A8_RW32(r)::"memory");
 }
+
+// Store 16 or 32 consecutive 32-bit columns of this thread's tensor-memory
+// lane; done (for this thread) after tmem_wait_store.
+__device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store_32cols(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Named barrier among `count` threads (a multiple of 32) of the CTA.
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) {
