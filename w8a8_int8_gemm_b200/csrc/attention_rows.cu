@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attention_rows_kernel(const At
 
   // Rows g and g + 8 of this lane: token in the document, key limit, place.
   int limit[2];
-  float place[2], slope[2];
+  int place[2];
+  float slope[2];
   uint4 qf[2][kChunks];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attention_rows_kernel(const At
     const int i = r / p.group;
     const int head = kv_head * p.group + r % p.group;
     limit[h] = live ? key_limit(p, doc, i) : 0;
-    place[h] = static_cast<float>(i + doc.shift);
+    place[h] = i + doc.shift;
     slope[h] = (BIAS && live) ? __ldg(p.slopes + head) * kLog2e : 0.0f;
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) attention_rows_kernel(const At
         const int h = x >> 1;
         const int j = key0 + 8 * a + 2 * t + (x & 1);
         float y = CAP ? capped(s[a][x], c_tanh, c_cap) : s[a][x] * c_scale;
-        if (BIAS) y -= slope[h] * fabsf(place[h] - static_cast<float>(j));
+        if (BIAS) y -= slope[h] * fabsf(static_cast<float>(place[h] - j));
         s[a][x] = j < limit[h] ? y : -INFINITY;
         top[h] = fmaxf(top[h], s[a][x]);
       }

@@ -45,6 +45,7 @@ constexpr int kRegsSoftmax = 208;     // 256 * 208 + 128 * 88 = 384 * 168, the r
 constexpr int kRegsOther = 88;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 64 values
 constexpr int kBarrierBytes = 256;
+constexpr int kFma = 6;               // pairs of 16 whose exponentials run on the FMA units
 constexpr float kGrowth = 8.0f;       // log2 of the growth of a row's maximum that rescales O
 
 __host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBlockBytes; }
@@ -71,10 +72,45 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t both(float a) { return pair(a, a); }
+
+// tanh(y) = y * sum_n kTanh[n] y^2n on [-1, 1]: least squares on Chebyshev nodes, relative error 7e-7 in binary32.
+__device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
+                                       -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
+
+// Maximum of three; NaN if one is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// 2^x of a pair on the FMA and integer units, for x in [-126, 127] (below:
+// 2^-126): x = n + f with n the nearest integer (read from the low bits of x +
+// 1.5 * 2^23) and |f| <= 1/2, 2^f by a polynomial of degree 5 (the minimax fit
+// of its relative error: 7.7e-8, 2.1e-7 as evaluated in binary32), and n added
+// to the exponent.
+__device__ __forceinline__ void ex2_pair_fma(uint64_t x, float& e0, float& e1) {
+  float x0, x1;
+  unpair(x, x0, x1);
+  x = pair(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
+  const uint64_t shifted = add2(x, both(12582912.0f));
+  const uint64_t f = fma2(add2(shifted, both(-12582912.0f)), both(-1.0f), x);
+  uint64_t y = fma2(f, both(1.3277938903e-3f), both(9.6757576406e-3f));
+  y = fma2(y, f, both(5.5507095981e-2f));
+  y = fma2(y, f, both(2.4022114338e-1f));
+  y = fma2(y, f, both(6.9314696823e-1f));
+  y = fma2(y, f, both(1.0000000733f));
+  float n0, n1, y0, y1;
+  unpair(shifted, n0, n1);
+  unpair(y, y0, y1);
+  e0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(n0) << 23));
+  e1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(n1) << 23));
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -100,13 +136,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;   // [2]
   uint64_t* s_full = q_full + 2;        // [2]
-  uint64_t* p_full = s_full + 2;        // [2]
-  uint64_t* o_full = p_full + 2;        // [2]
+  uint64_t* p_full = s_full + 2;        // [2][2], for the first and second 64 keys of a tile
+  uint64_t* o_full = p_full + 4;        // [2]
   uint64_t* drain = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // (known to be uniform)
   const int lane = threadIdx.x & 31;
 
   // Causal documents: the slots with the most keys first, so that the last CTAs to start are short ones.
@@ -138,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[2 * s], 4);
+      mbar_init(&p_full[2 * s + 1], 4);
       mbar_init(&o_full[s], 1);
     }
     mbar_init(drain, 1);
@@ -216,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait_fill(2 * j);
         if (!ok) return;
         tc_fence_after_sync();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint32_t q = smem_u32(sQ + s * kTile);
           const uint32_t k = smem_u32(ring + (2 * j % kStages) * kTile);
 #pragma unroll
@@ -237,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&q_full[1], 0, kSiteAttnOperand);
         scores(1, 0);
       }
-      if (ok && tiles > 0 && lane == 0) mma_commit(&empty[0]);
+      if (ok && tiles > 0 && elect_one()) mma_commit(&empty[0]);
       __syncwarp();
       for (int j = 0; ok && j < tiles; ++j) {
         const int vf = 2 * j + 1;
@@ -257,30 +294,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
           const int n = s == 0 ? n0 : n1;
           if (j >= n) continue;
-          wait(&p_full[s], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (lane == 0) {
-            const uint32_t v = smem_u32(ring + (vf % kStages) * kTile);
 #pragma unroll
-            for (int x = 0; x < kTileK / 16; ++x) {
-              mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x,
-                          make_smem_desc_n_sw128(v + x * 16 * 128, kBlockBytes), kIdescO, (j > 0 || x > 0) ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            wait(&p_full[2 * s + h], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
+            if (!ok) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
+              const uint32_t v = smem_u32(ring + (vf % kStages) * kTile);
+#pragma unroll
+              for (int x = 4 * h; x < 4 * h + 4; ++x) {
+                mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x,
+                            make_smem_desc_n_sw128(v + x * 16 * 128, kBlockBytes), kIdescO,
+                            (j > 0 || x > 0) ? 1u : 0u);
+              }
+              if (h == 1 && j + 1 == n) mma_commit(&o_full[s]);
             }
-            if (j + 1 == n) mma_commit(&o_full[s]);
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
           if (j + 1 < n) scores(s, j + 1);
           if (!ok) break;
         }
-        if (ok && lane == 0) {
+        if (ok && elect_one()) {
           mma_commit(&empty[vf % kStages]);
           if (j + 1 < tiles) mma_commit(&empty[(vf + 1) % kStages]);
         }
         __syncwarp();
       }
       // No MMA may still run when tensor memory is freed.
-      if (lane == 0) {
+      if (elect_one()) {
         mma_commit(drain);
         mbar_wait_drain(drain, 0, p.timeout_ns, err);
       }
@@ -302,10 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int least = my_rows > 0 ? key_limit(p, doc, row0 + s * kSub) : 0;  // the sub-tile's smallest limit
     constexpr bool kChange = CAP || BIAS;  // scores need more than the factor c
     const float c = p.scale * kLog2e;
-    const float c_tanh = CAP ? 2.0f * kLog2e * p.scale / p.cap : 0.0f;
+    const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
+    const float c_tanh = 2.0f * kLog2e * inv_cap;
     const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
     const float slope = BIAS ? __ldg(p.slopes + head) * kLog2e : 0.0f;
-    const float place = static_cast<float>(i + doc.shift);
+    const int place = i + doc.shift;
+    const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
 
     float m = -INFINITY;  // in units of log2
     float l = 0.0f;
@@ -320,19 +364,69 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 4; ++b) tmem_wait_load(v[b]);
 
-      if constexpr (kChange) {
+      if constexpr (CAP) {
+        // Scores within the cap on either side (all of them, unless the scores are far beyond it) take an odd
+        // polynomial for tanh on [-1, 1]; others two special functions each.
+        float far = 0.0f;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            float y = __uint_as_float(v[b][x]);
-            y = CAP ? capped(y, c_tanh, c_cap) : y * c;
-            if (BIAS) y -= slope * fabsf(place - static_cast<float>(j * kTileK + 32 * b + x));
-            v[b][x] = __float_as_uint(y);
+          for (int x = 0; x < 32; x += 2) {
+            far = max3(far, fabsf(__uint_as_float(v[b][x])), fabsf(__uint_as_float(v[b][x + 1])));
+          }
+        }
+        if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const uint64_t y = mul2(pair(__uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1])), both(inv_cap));
+              const uint64_t u = mul2(y, y);
+              uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
+              t = fma2(t, u, both(kTanh[3]));
+              t = fma2(t, u, both(kTanh[2]));
+              t = fma2(t, u, both(kTanh[1]));
+              t = fma2(t, u, both(kTanh[0]));
+              float a0, a1;
+              unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
+              v[b][x] = __float_as_uint(a0);
+              v[b][x + 1] = __float_as_uint(a1);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[b][x] = __float_as_uint(capped(__uint_as_float(v[b][x]), c_tanh, c_cap));
           }
         }
       }
-      if ((j + 1) * kTileK > least) {
+      if constexpr (BIAS) {
+        const float f = CAP ? 1.0f : c;
+        const float first = static_cast<float>(j * kTileK - place);  // distance of the tile's first key, signed
+        if ((j + 1) * kTileK <= first_place + 1) {
+          // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
+          const float at0 = slope * first;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              v[b][x] = __float_as_uint(fmaf(__uint_as_float(v[b][x]), f, fmaf(slope, static_cast<float>(32 * b + x), at0)));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              v[b][x] = __float_as_uint(
+                  fmaf(__uint_as_float(v[b][x]), f, -slope * fabsf(first + static_cast<float>(32 * b + x))));
+            }
+          }
+        }
+      }
+      const bool masked = (j + 1) * kTileK > least;
+      if (masked) {
         const int left = limit - j * kTileK;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -342,17 +436,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      float top = -INFINITY;
+      float tops[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
+        tops[b] = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) top = max3(top, __uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1]));
+        for (int x = 0; x < 32; x += 2) {
+          tops[b] = max3(tops[b], __uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1]));
+        }
       }
+      float top = max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[3]);
       if (!kChange) top *= c;  // c > 0
       if (j == 0) {
         m = top;
       } else {
-        const bool grow = top > m + kGrowth;
+        const bool grow = !(top <= m + kGrowth);  // (a NaN reaches O and l, and stays there)
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float f = grow ? ex2(m - top) : 1.0f;
           if (grow) m = top;
@@ -368,30 +466,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
-      const uint64_t c2 = pair(kChange ? 1.0f : c, kChange ? 1.0f : c), minus = pair(-base, -base);
-      uint64_t sum = pair(0.0f, 0.0f);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
+      const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
+      // Weights of 32 keys.  In whole tiles kFma of every 16 pairs take their exponentials on the FMA units, which
+      // the special-function units alone would hold up; masked tiles need 2^-inf = 0.
+      uint64_t sums[2] = {both(0.0f), both(0.0f)};
+      auto weights = [&](int b, bool mixed) {
         uint32_t w[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const uint64_t y = pair(__uint_as_float(v[b][2 * x]), __uint_as_float(v[b][2 * x + 1]));
+          const uint64_t e = kChange ? add2(y, minus) : fma2(y, c2, minus);
           float a0, a1;
-          unpair(kChange ? add2(y, minus) : fma2(y, c2, minus), a0, a1);
-          a0 = ex2(a0);
-          a1 = ex2(a1);
-          sum = add2(sum, pair(a0, a1));
+          if (mixed && x * kFma / 16 != (x + 1) * kFma / 16) {
+            ex2_pair_fma(e, a0, a1);
+          } else {
+            unpair(e, a0, a1);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+          }
+          sums[x & 1] = add2(sums[x & 1], pair(a0, a1));
           w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
         }
         tmem_store_16cols(t_s + 16 * b, w);
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (masked) {
+          weights(2 * h, false);
+          weights(2 * h + 1, false);
+        } else {
+          weights(2 * h, true);
+          weights(2 * h + 1, true);
+        }
+        tmem_wait_store();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * s + h]);
       }
       float s0, s1;
-      unpair(sum, s0, s1);
+      unpair(add2(sums[0], sums[1]), s0, s1);
       l += s0 + s1;
-      tmem_wait_store();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
     }
 
     // ------------------------------------------------------------- epilogue

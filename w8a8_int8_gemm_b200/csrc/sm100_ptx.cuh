@@ -32,6 +32,20 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in one lane of a converged warp, always the same one.  Unlike a
+// comparison of the lane number, the compiler knows that a branch on it runs
+// one lane, and keeps the operands of single-thread instructions (tcgen05.mma
+// descriptors) in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -79,13 +93,17 @@ __device__ __forceinline__ void record_timeout(int* err, int site) { atomicCAS(e
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                   uint64_t timeout_ns, int* err, int site) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait(a, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
+  // The timer is read only once the wait has lasted a while: a read takes
+  // longer than most waits of a pipeline.
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(a, parity)) return true;
     if ((i & 31u) == 0) {
       if (*abort) return false;
-      if (global_timer_ns() - t0 > timeout_ns) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > timeout_ns) {
         record_timeout(err, site);
         *abort = 1;
         return false;
