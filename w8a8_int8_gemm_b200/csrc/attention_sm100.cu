@@ -11,13 +11,15 @@
 // than 2^8 since m was last set (P then reaches 2^8 at most, and the sum is
 // binary32), so in most tiles no thread touches it.
 //
-//   warps 0-3, 4-7  softmax of sub-tile 0 / 1; a thread owns a query, so
-//                   maximum and sum need no exchange
-//   warp 8          loads Q, then K and V tiles through a ring (TMA)
-//   warp 9          issues the MMAs: while one sub-tile's softmax runs, the
-//                   tensor cores work for the other; it also zeroes the
-//                   rows of the last V tile that lie behind the document's
-//                   end (a weight of 0 times whatever is there must be 0)
+//   warps 0-7, 8-15 softmax of sub-tile 0 / 1: a query's 128 scores of a
+//                   tile belong to two threads, 64 each, which exchange
+//                   their maximum through shared memory
+//   warp 16         loads Q, then K and V tiles through a ring (TMA)
+//   warp 17         issues the MMAs: while one sub-tile's softmax runs, the
+//                   tensor cores work for the other
+//   warp 18         zeroes the rows of the last V tile that lie behind the
+//                   document's end (a weight of 0 times whatever is there
+//                   must be 0)
 //
 // The tensor cores execute MMAs in the order they are issued, so S of tile
 // j + 1 may overwrite P of tile j right behind O += P V, and "S full" also
@@ -40,18 +42,22 @@ namespace {
 constexpr int kSub = 128;             // queries of a sub-tile
 constexpr int kTileQ = 2 * kSub;      // queries of a CTA
 constexpr int kTileK = 128;           // keys of a tile
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208;     // 256 * 208 + 128 * 88 = 384 * 168, the registers the CTA starts with
-constexpr int kRegsOther = 88;
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * kSoftmaxWarps + 128;
+constexpr int kRegsSoftmax = 104;     // 512 * 104 + 128 * 64 = 640 * 96, the registers the CTA starts with
+constexpr int kRegsOther = 64;
 constexpr int kBlockBytes = 128 * 128;  // 128 rows x 64 values
-constexpr int kBarrierBytes = 256;
-constexpr int kFma = 6;               // pairs of 16 whose exponentials run on the FMA units
+// A float per query and half of the keys (the softmax threads' exchange) and the barriers, in front of Q and the ring,
+// which are aligned to 1024 bytes: at D = 128 all of the 227 KB.
+constexpr int kExchange = 2 * 2 * kSub;
+constexpr int kHeadBytes = 3 * 1024;
+constexpr int kFma = 4;               // pairs of 16 whose exponentials run on the FMA units
 constexpr float kGrowth = 8.0f;       // log2 of the growth of a row's maximum that rescales O
 
 __host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBlockBytes; }
 __host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 5 : 8; }
 __host__ __device__ constexpr int smem_bytes(int D) {
-  return 1024 + (2 + ring_stages(D)) * tile_bytes(D) + kBarrierBytes;
+  return kHeadBytes + (2 + ring_stages(D)) * tile_bytes(D);
 }
 
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -87,6 +93,12 @@ __device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.32
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -128,17 +140,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdescO = make_idesc_bf16(kSub, D, true);
   constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 columns each), O0, O1 (D each)
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* exchange = reinterpret_cast<float*>(smem);  // [half][sub-tile][query]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kExchange * sizeof(float));
+  uint8_t* sQ = smem + kHeadBytes;
   uint8_t* ring = sQ + 2 * kTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kStages * kTile);
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;   // [2]
   uint64_t* s_full = q_full + 2;        // [2]
-  uint64_t* p_full = s_full + 2;        // [2][2], for the first and second 64 keys of a tile
-  uint64_t* o_full = p_full + 4;        // [2]
-  uint64_t* drain = o_full + 2;
+  uint64_t* p_full = s_full + 2;        // [2]
+  uint64_t* o_full = p_full + 2;        // [2]
+  uint64_t* tail_full = o_full + 2;
+  uint64_t* drain = tail_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -166,6 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tail_rows = doc.lk - (tiles - 1) * kTileK;  // rows of the last V tile that are the document's
   const bool tail = tiles > 0 && tail_rows < kTileK;
 
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it; a kernel without static shared memory has it
+    if (threadIdx.x == 0) record_timeout(err, kSiteAttnLoad);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -174,20 +191,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[2 * s], 4);
-      mbar_init(&p_full[2 * s + 1], 4);
+      mbar_init(&p_full[s], kSoftmaxWarps / 2);
       mbar_init(&o_full[s], 1);
     }
+    mbar_init(tail_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 16 && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish_alloc_permit();
   }
@@ -196,143 +213,146 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp >= 8) {
+  if (warp >= kSoftmaxWarps) {
     reg_lower<kRegsOther>();
-    if (warp == 8) {
+    // One thread each: a warp that votes, elects and converges around every wait spends most of a tile's time on
+    // that (measured: 4 300 cycles a tile of 256 x 128 x 128, of which the issuing warp was idle in none).
+    const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+      return mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
+    };
+    if (warp == 16 && elect_one()) {
       // ------------------------------------------------------------ loader
       const uint64_t keep = l2_policy_evict_last();
       const uint64_t once = l2_policy_evict_first();
       int fills = 0;
-      int q_loads = 0;
-      bool ok = true;
-      auto load_q = [&](int s) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&q_full[s], kTile);
-          for (int b = 0; b < kBlocks; ++b) {
-            tma_load_3d_hint(sQ + s * kTile + b * kBlockBytes, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub,
-                             head, once);
-          }
+      const auto load_q = [&](int s) {
+        mbar_arrive_expect_tx(&q_full[s], kTile);
+        for (int b = 0; b < kBlocks; ++b) {
+          tma_load_3d_hint(sQ + s * kTile + b * kBlockBytes, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub, head,
+                           once);
         }
-        __syncwarp();
-        ++q_loads;
       };
       if (n0 > 0) load_q(0);
+      if (n1 > 0) load_q(1);
+      int stage = 0;
+      uint32_t phase = 1;
       for (int f = 0; f < 2 * tiles; ++f) {
-        const int stage = f % kStages;
-        ok = warp_wait(&empty[stage], static_cast<uint32_t>((f / kStages) & 1) ^ 1u, abort_flag, p.timeout_ns, err,
-                       kSiteAttnLoad);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&full[stage], kTile);
-          for (int b = 0; b < kBlocks; ++b) {
-            tma_load_3d_hint(ring + stage * kTile + b * kBlockBytes, (f & 1) ? &tm_v : &tm_k, &full[stage], 64 * b,
-                             doc.k0 + (f >> 1) * kTileK, kv_head, keep);
-          }
+        if (!wait(&empty[stage], phase, kSiteAttnLoad)) break;
+        // (a last V tile that ends inside goes to warp 18 first, which fills the slot)
+        uint64_t* landed = tail && f == 2 * tiles - 1 ? tail_full : &full[stage];
+        mbar_arrive_expect_tx(landed, kTile);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+          tma_load_3d_hint(ring + stage * kTile + b * kBlockBytes, (f & 1) ? &tm_v : &tm_k, landed, 64 * b,
+                           doc.k0 + (f >> 1) * kTileK, kv_head, keep);
         }
-        __syncwarp();
         ++fills;
-        if (f == 0 && n1 > 0) load_q(1);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
       // Every load must have landed before the CTA ends (on the normal path they have).
-      if (lane == 0) {
-        for (int f = max(0, fills - kStages); f < fills; ++f) {
-          mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
+      for (int f = max(0, fills - kStages); f < fills; ++f) {
+        if (tail && f == 2 * tiles - 1) {
+          mbar_wait_drain(tail_full, 0, p.timeout_ns, err);
+          continue;
         }
-        if (n0 > 0) mbar_wait_drain(&q_full[0], 0, p.timeout_ns, err);
-        if (q_loads > (n0 > 0 ? 1 : 0)) mbar_wait_drain(&q_full[1], 0, p.timeout_ns, err);
+        mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
       }
-      __syncwarp();
-    } else if (warp == 9) {
+      if (n0 > 0) mbar_wait_drain(&q_full[0], 0, p.timeout_ns, err);
+      if (n1 > 0) mbar_wait_drain(&q_full[1], 0, p.timeout_ns, err);
+    } else if (warp == 17 && elect_one()) {
       // -------------------------------------------------------- MMA issuer
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-        if (ok) ok = warp_wait(bar, parity, abort_flag, p.timeout_ns, err, site);
-      };
-      auto wait_fill = [&](int f) { wait(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), kSiteAttnOperand); };
-      auto scores = [&](int s, int j) {  // S_s = Q_s K_j^T
-        wait_fill(2 * j);
-        if (!ok) return;
-        tc_fence_after_sync();
-        if (elect_one()) {
-          const uint32_t q = smem_u32(sQ + s * kTile);
-          const uint32_t k = smem_u32(ring + (2 * j % kStages) * kTile);
+      // Matrix descriptors: the high words are constant, the low ones hold the address (in units of 16 bytes).
+      const uint64_t desc_k = make_smem_desc_k_sw128(0), desc_v = make_smem_desc_n_sw128(0, kBlockBytes);
+      const uint32_t q_addr = smem_u32(sQ) >> 4, ring_addr = smem_u32(ring) >> 4;
+      constexpr uint32_t kTile16 = kTile / 16, kBlock16 = kBlockBytes / 16;
+      // S_s = Q_s K^T with K in ring slot `stage`
+      const auto scores = [&](int s, int stage) {
+        const uint64_t qd = desc_k + (q_addr + s * kTile16), kd = desc_k + (ring_addr + stage * kTile16);
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = (x / 4) * kBlockBytes;
-            mma_bf16_ss(tmem + s * kTileK, make_smem_desc_k_sw128(q + off) + 2 * (x % 4),
-                        make_smem_desc_k_sw128(k + off) + 2 * (x % 4), kIdescS, x > 0);
-          }
-          mma_commit(&s_full[s]);
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = (x / 4) * kBlock16 + 2 * (x % 4);
+          mma_bf16_ss(tmem + s * kTileK, qd + off, kd + off, kIdescS, x > 0);
         }
-        __syncwarp();
+        mma_commit(&s_full[s]);
       };
-      if (n0 > 0) {
-        wait(&q_full[0], 0, kSiteAttnOperand);
-        scores(0, 0);
+      if (tiles > 0) ok = wait(&full[0], 0, kSiteAttnOperand);
+#pragma unroll 1
+      for (int s = 0; ok && s < 2; ++s) {
+        if ((s == 0 ? n0 : n1) == 0) continue;
+        ok = wait(&q_full[s], 0, kSiteAttnOperand);
+        if (ok) scores(s, 0);
       }
-      if (n1 > 0) {
-        wait(&q_full[1], 0, kSiteAttnOperand);
-        scores(1, 0);
-      }
-      if (ok && tiles > 0 && elect_one()) mma_commit(&empty[0]);
-      __syncwarp();
+      if (ok && tiles > 0) mma_commit(&empty[0]);
+      int v_stage = 1;
+      uint32_t v_phase = 0;
       for (int j = 0; ok && j < tiles; ++j) {
-        const int vf = 2 * j + 1;
-        wait_fill(vf);
-        if (!ok) break;
-        if (tail && j == tiles - 1) {
-          uint8_t* v = ring + (vf % kStages) * kTile;
-          for (int x = tail_rows * 8 + lane; x < kTileK * 8; x += 32) {
-#pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-              *reinterpret_cast<uint4*>(v + b * kBlockBytes + x * 16) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
+        int k_stage = v_stage + 1;  // of tile j + 1
+        uint32_t k_phase = v_phase;
+        if (k_stage == kStages) {
+          k_stage = 0;
+          k_phase ^= 1u;
         }
+        ok = wait(&full[v_stage], v_phase, kSiteAttnOperand) &&
+             (j + 1 == tiles || wait(&full[k_stage], k_phase, kSiteAttnOperand));
+        if (!ok) break;
+#pragma unroll 1
         for (int s = 0; s < 2; ++s) {
           const int n = s == 0 ? n0 : n1;
           if (j >= n) continue;
+          ok = wait(&p_full[s], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t vd = desc_v + (ring_addr + v_stage * kTile16);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            wait(&p_full[2 * s + h], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
-            if (!ok) break;
-            tc_fence_after_sync();
-            if (elect_one()) {
-              const uint32_t v = smem_u32(ring + (vf % kStages) * kTile);
-#pragma unroll
-              for (int x = 4 * h; x < 4 * h + 4; ++x) {
-                mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x,
-                            make_smem_desc_n_sw128(v + x * 16 * 128, kBlockBytes), kIdescO,
-                            (j > 0 || x > 0) ? 1u : 0u);
-              }
-              if (h == 1 && j + 1 == n) mma_commit(&o_full[s]);
-            }
-            __syncwarp();
+          for (int x = 0; x < kTileK / 16; ++x) {
+            mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x, vd + 128 * x, kIdescO,
+                        (x > 0 || j > 0) ? 1u : 0u);
           }
-          if (!ok) break;
-          if (j + 1 < n) scores(s, j + 1);
-          if (!ok) break;
+          if (j + 1 < n) {
+            scores(s, k_stage);
+          } else {
+            mma_commit(&o_full[s]);
+          }
         }
-        if (ok && elect_one()) {
-          mma_commit(&empty[vf % kStages]);
-          if (j + 1 < tiles) mma_commit(&empty[(vf + 1) % kStages]);
+        if (!ok) break;
+        mma_commit(&empty[v_stage]);
+        if (j + 1 < tiles) mma_commit(&empty[k_stage]);
+        v_stage = k_stage + 1;
+        v_phase = k_phase;
+        if (v_stage == kStages) {
+          v_stage = 0;
+          v_phase ^= 1u;
         }
-        __syncwarp();
       }
       // No MMA may still run when tensor memory is freed.
-      if (elect_one()) {
-        mma_commit(drain);
-        mbar_wait_drain(drain, 0, p.timeout_ns, err);
+      mma_commit(drain);
+      mbar_wait_drain(drain, 0, p.timeout_ns, err);
+    } else if (warp == 18 && tail) {
+      // ------------------------------------------------ end of the document
+      const int stage = (2 * tiles - 1) % kStages;
+      if (warp_wait(tail_full, 0, abort_flag, p.timeout_ns, err, kSiteAttnOperand)) {
+        uint8_t* v = ring + stage * kTile;
+        for (int x = tail_rows * 8 + lane; x < kTileK * 8; x += 32) {
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4*>(v + b * kBlockBytes + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
       }
       __syncwarp();
+      if (lane == 0) mbar_arrive(&full[stage]);
     }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     reg_raise<kRegsSoftmax>();
-    const int s = warp >> 2;
+    const int s = warp >> 3;
+    const int part = (warp >> 2) & 1;  // keys 64 part .. 64 part + 63 of every tile
     const int quarter = warp & 3;
+    const uint32_t partners = 1 + (warp >> 3) * 4 + quarter;  // named barrier of the two warps of 32 queries
     const int my_rows = min(kSub, rows - s * kSub);  // <= 0: nothing in this sub-tile
     const int n = s == 0 ? n0 : n1;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -351,6 +371,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int place = i + doc.shift;
     const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
 
+    // 32 scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
+    auto first_pass = [&](uint32_t (&v)[32], int key0, bool masked) {
+      if constexpr (CAP) {
+        // Scores within the cap on either side (all of them, unless the scores are far beyond it) take the
+        // polynomial for tanh; others two special functions each.
+        float far = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
+        if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const uint64_t y = mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), both(inv_cap));
+            const uint64_t u = mul2(y, y);
+            uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
+            t = fma2(t, u, both(kTanh[3]));
+            t = fma2(t, u, both(kTanh[2]));
+            t = fma2(t, u, both(kTanh[1]));
+            t = fma2(t, u, both(kTanh[0]));
+            float a0, a1;
+            unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
+            v[x] = __float_as_uint(a0);
+            v[x + 1] = __float_as_uint(a1);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
+        }
+      }
+      if constexpr (BIAS) {
+        const float f = CAP ? 1.0f : c;
+        const float first = static_cast<float>(key0 - place);  // distance of the first key, signed
+        if (key0 + 31 <= first_place) {
+          // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
+          const float at0 = slope * first;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, fmaf(slope, static_cast<float>(x), at0)));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, -slope * fabsf(first + static_cast<float>(x))));
+          }
+        }
+      }
+      if (masked) {
+        const int left = limit - key0;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          if (x >= left) v[x] = 0xFF800000u;  // -inf
+        }
+      }
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < 32; x += 4) {
+        top[0] = max3(top[0], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+        top[1] = max3(top[1], __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+      }
+      return fmax_nan(top[0], top[1]);
+    };
+
+    // The value of the thread with the other 64 keys of this query.  One barrier is enough: a thread writes its
+    // next value when the MMAs that wait for its partner's weights are done, so after the partner read this one.
+    float* const mine = exchange + (part * 2 + s) * kSub + in_sub;
+    const float* const other = exchange + ((part ^ 1) * 2 + s) * kSub + in_sub;
+    const auto partner = [&](float x) {
+      *mine = x;
+      named_barrier_sync(partners, 64);
+      return *other;
+    };
+
     float m = -INFINITY;  // in units of log2
     float l = 0.0f;
     bool ok = true;
@@ -358,123 +449,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&s_full[s], static_cast<uint32_t>(j & 1), abort_flag, p.timeout_ns, err, kSiteAttnScores);
       if (!ok) break;
       tc_fence_after_sync();
-      uint32_t v[4][32];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_load_32cols_async(t_s + 32 * b, v[b]);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_wait_load(v[b]);
-
-      if constexpr (CAP) {
-        // Scores within the cap on either side (all of them, unless the scores are far beyond it) take an odd
-        // polynomial for tanh on [-1, 1]; others two special functions each.
-        float far = 0.0f;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            far = max3(far, fabsf(__uint_as_float(v[b][x])), fabsf(__uint_as_float(v[b][x + 1])));
-          }
-        }
-        if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const uint64_t y = mul2(pair(__uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1])), both(inv_cap));
-              const uint64_t u = mul2(y, y);
-              uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
-              t = fma2(t, u, both(kTanh[3]));
-              t = fma2(t, u, both(kTanh[2]));
-              t = fma2(t, u, both(kTanh[1]));
-              t = fma2(t, u, both(kTanh[0]));
-              float a0, a1;
-              unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
-              v[b][x] = __float_as_uint(a0);
-              v[b][x + 1] = __float_as_uint(a1);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[b][x] = __float_as_uint(capped(__uint_as_float(v[b][x]), c_tanh, c_cap));
-          }
-        }
-      }
-      if constexpr (BIAS) {
-        const float f = CAP ? 1.0f : c;
-        const float first = static_cast<float>(j * kTileK - place);  // distance of the tile's first key, signed
-        if ((j + 1) * kTileK <= first_place + 1) {
-          // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
-          const float at0 = slope * first;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              v[b][x] = __float_as_uint(fmaf(__uint_as_float(v[b][x]), f, fmaf(slope, static_cast<float>(32 * b + x), at0)));
-            }
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              v[b][x] = __float_as_uint(
-                  fmaf(__uint_as_float(v[b][x]), f, -slope * fabsf(first + static_cast<float>(32 * b + x))));
-            }
-          }
-        }
-      }
       const bool masked = (j + 1) * kTileK > least;
-      if (masked) {
-        const int left = limit - j * kTileK;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            if (32 * b + x >= left) v[b][x] = 0xFF800000u;  // -inf
-          }
-        }
-      }
-      float tops[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        tops[b] = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          tops[b] = max3(tops[b], __uint_as_float(v[b][x]), __uint_as_float(v[b][x + 1]));
-        }
-      }
-      float top = max3(max3(tops[0], tops[1], tops[2]), tops[3], tops[3]);
+      const int key0 = j * kTileK + 64 * part;
+      uint32_t va[32], vb[32];
+      tmem_load_32cols_async(t_s + 64 * part, va);
+      tmem_load_32cols_async(t_s + 64 * part + 32, vb);
+      tmem_wait_load(va);
+      tmem_wait_load(vb);
+      float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
+      // The partner's maximum.  (Behind the barrier both have read their scores, and P may be written over them.)
+      tc_fence_before_sync();
+      top = fmax_nan(top, partner(top));
+      tc_fence_after_sync();
       if (!kChange) top *= c;  // c > 0
       if (j == 0) {
         m = top;
       } else {
         const bool grow = !(top <= m + kGrowth);  // (a NaN reaches O and l, and stays there)
-        if (__any_sync(0xFFFFFFFFu, grow)) {
+        if (__any_sync(0xFFFFFFFFu, grow)) {      // (the same in both warps)
           const float f = grow ? ex2(m - top) : 1.0f;
           if (grow) m = top;
           l *= f;
-#pragma unroll
+#pragma unroll 1
           for (int b = 0; b < D / 32; ++b) {
-            uint32_t o[32];
-            tmem_load_32cols(t_o + 32 * b, o);
+            uint32_t o[16];
+            tmem_load_16cols(t_o + D / 2 * part + 16 * b, o);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_store_32cols(t_o + 32 * b, o);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+            tmem_store_16cols(t_o + D / 2 * part + 16 * b, o);
           }
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
       const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
-      // Weights of 32 keys.  In whole tiles kFma of every 16 pairs take their exponentials on the FMA units, which
-      // the special-function units alone would hold up; masked tiles need 2^-inf = 0.
       uint64_t sums[2] = {both(0.0f), both(0.0f)};
-      auto weights = [&](int b, bool mixed) {
+      // Weights of 32 keys.  In whole tiles kFma of every 16 pairs take their exponentials on the FMA units; masked
+      // tiles need 2^-inf = 0.
+      auto weights = [&](const uint32_t (&v)[32], int b, bool mixed) {
         uint32_t w[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          const uint64_t y = pair(__uint_as_float(v[b][2 * x]), __uint_as_float(v[b][2 * x + 1]));
+          const uint64_t y = pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
           const uint64_t e = kChange ? add2(y, minus) : fma2(y, c2, minus);
           float a0, a1;
           if (mixed && x * kFma / 16 != (x + 1) * kFma / 16) {
@@ -487,22 +502,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           sums[x & 1] = add2(sums[x & 1], pair(a0, a1));
           w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
         }
-        tmem_store_16cols(t_s + 16 * b, w);
+        tmem_store_16cols(t_s + 32 * part + 16 * b, w);
       };
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (masked) {
-          weights(2 * h, false);
-          weights(2 * h + 1, false);
-        } else {
-          weights(2 * h, true);
-          weights(2 * h + 1, true);
-        }
-        tmem_wait_store();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * s + h]);
+      if (kFma == 0 || masked) {
+        weights(va, 0, false);
+        weights(vb, 1, false);
+      } else {
+        weights(va, 0, true);
+        weights(vb, 1, true);
       }
+      tmem_wait_store();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
       float s0, s1;
       unpair(add2(sums[0], sums[1]), s0, s1);
       l += s0 + s1;
@@ -510,33 +522,34 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ------------------------------------------------------------- epilogue
     if (ok && n > 0) ok = warp_wait(&o_full[s], 0, abort_flag, p.timeout_ns, err, kSiteAttnOut);
+    if (!ok) named_barrier_arrive(partners, 64);  // the partner may stand at its barrier: it will see the abort next
     if (ok && my_rows > 0) {
       tc_fence_after_sync();
+      l += partner(l);
       const bool any = limit > 0;
       const float inv = any ? 1.0f / l : 0.0f;
-      // The warp's 32 rows through shared memory (its part of the sub-tile's Q, which no MMA reads any more),
-      // so that a row leaves in whole 128-byte lines.
-      constexpr int kRowBytes = 2 * D;
-      constexpr int kVec = kRowBytes / 16;
-      uint8_t* stage = sQ + s * kTile + quarter * 32 * kRowBytes;
-#pragma unroll
+      // The warp's 32 rows x D/2 values through shared memory (its part of the sub-tile's Q, which no MMA reads any
+      // more), so that they leave in whole segments of D bytes.
+      constexpr int kVec = D / 16;  // 16-byte vectors of a row
+      uint8_t* stage = sQ + s * kTile + (part * 4 + quarter) * 32 * D;
+#pragma unroll 1
       for (int b = 0; b < D / 32; ++b) {
-        uint32_t o[32];
+        uint32_t o[16];
         if (n > 0) {
-          tmem_load_32cols(t_o + 32 * b, o);
+          tmem_load_16cols(t_o + D / 2 * part + 16 * b, o);
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0u;
+          for (int x = 0; x < 16; ++x) o[x] = 0u;
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 2; ++x) {
           uint32_t w[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const float a0 = __uint_as_float(o[8 * x + 2 * y]) * inv, a1 = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
             w[y] = any ? pack_bf16(a0, a1) : 0u;
           }
-          *reinterpret_cast<uint4*>(stage + lane * kRowBytes + (((4 * b + x) ^ (lane & 7)) * 16)) =
+          *reinterpret_cast<uint4*>(stage + lane * D + (((2 * b + x) ^ (lane & (kVec - 1))) * 16)) =
               make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
@@ -547,11 +560,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = lane; e < 32 * kVec; e += 32) {
         const int r = e / kVec, x = e % kVec;
         if (r < valid) {
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((x ^ (r & 7)) * 16));
-          *reinterpret_cast<uint4*>(p.out + (token0 + r) * p.ldo + head * p.hso + x * 8) = w;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * D + ((x ^ (r & (kVec - 1))) * 16));
+          *reinterpret_cast<uint4*>(p.out + (token0 + r) * p.ldo + head * p.hso + D / 2 * part + x * 8) = w;
         }
       }
-      if (p.lse != nullptr && in_sub < my_rows) {
+      if (p.lse != nullptr && part == 0 && in_sub < my_rows) {
         p.lse[(token0 + lane) * p.heads_q + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
     }
@@ -568,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -608,6 +621,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
+  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 10) * 8 + 8 <= kHeadBytes, "shared memory");
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t slots = p.tokens_q / kTileQ + p.docs;

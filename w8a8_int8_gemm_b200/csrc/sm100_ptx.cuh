@@ -86,18 +86,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 __device__ __forceinline__ void record_timeout(int* err, int site) { atomicCAS(err, 0, site); }
 
-// Wait until the phase with the given parity of `bar` has completed, for at
-// most timeout_ns.  Gives up early when *abort is set by another warp of
-// the CTA.  Returns false on timeout (recording `site` in the device error
-// word *err and raising *abort) or on abort.
-__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                  uint64_t timeout_ns, int* err, int site) {
-  const uint32_t a = smem_u32(bar);
-  // The timer is read only once the wait has lasted a while: a read takes
-  // longer than most waits of a pipeline.
+// The part of a bounded wait that polls.  The timer is read only once the
+// wait has lasted a while: a read takes longer than most waits of a pipeline.
+__device__ __forceinline__ bool mbar_wait_poll(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
+                                            int* err, int site) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(a, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if ((i & 31u) == 0) {
       if (*abort) return false;
       const uint64_t now = global_timer_ns();
@@ -110,6 +105,16 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
       }
     }
   }
+}
+
+// Wait until the phase with the given parity of `bar` has completed, for at
+// most timeout_ns.  Gives up early when *abort is set by another warp of
+// the CTA.  Returns false on timeout (recording `site` in the device error
+// word *err and raising *abort) or on abort.
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                  uint64_t timeout_ns, int* err, int site) {
+  const uint32_t a = smem_u32(bar);
+  return mbar_try_wait(a, parity) || mbar_wait_poll(a, parity, abort, timeout_ns, err, site);
 }
 
 // Same, without the abort check: used on the teardown path to let copies
@@ -569,6 +574,16 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : W8A8_RW32(r)::"memory");
 }
 
+// Load 16 consecutive 32-bit columns of this thread's lane and wait for them.
+__device__ __forceinline__ void tmem_load_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Store 16 or 32 consecutive 32-bit columns of this thread's tensor-memory
 // lane; done (for this thread) after tmem_wait_store.
 __device__ __forceinline__ void tmem_store_16cols(uint32_t taddr, const uint32_t (&v)[16]) {
@@ -585,6 +600,11 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 // Named barrier among `count` threads (a multiple of 32) of the CTA.
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// Arrive on a named barrier without waiting.
+__device__ __forceinline__ void named_barrier_arrive(uint32_t id, uint32_t count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // Load 32 consecutive 32-bit columns of this thread's tensor-memory lane
