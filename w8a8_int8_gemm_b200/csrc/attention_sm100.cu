@@ -2,32 +2,39 @@
 // tensor cores.
 //
 // A CTA takes 256 queries of one document and head, as two sub-tiles of 128
-// (the rows of a tcgen05.mma), and walks the keys 128 at a time:
+// (the rows of a tcgen05.mma), and walks the keys a tile at a time:
 //   S = Q K^T       Q and K from shared memory, S in tensor memory
-//   P = 2^(S c - m) rounded to bf16, written over S in tensor memory
+//   P = 2^(S c - m) rounded to bf16, in tensor memory
 //   O += P V        P from tensor memory, V from shared memory
 // with the running maximum m and sum of a softmax per query.  O stays in
 // tensor memory: it is rescaled only when a row's maximum has grown by more
 // than 2^8 since m was last set (P then reaches 2^8 at most, and the sum is
 // binary32), so in most tiles no thread touches it.
 //
-//   warps 0-7, 8-15 softmax of sub-tile 0 / 1: a query's 128 scores of a
-//                   tile belong to two threads, 64 each, which exchange
-//                   their maximum through shared memory
+//   warps 0-7, 8-15 softmax of sub-tile 0 / 1: a query's scores of a tile
+//                   belong to two threads, half of the keys each, which
+//                   exchange their maxima through shared memory
 //   warp 16         loads Q, then K and V tiles through a ring (TMA)
-//   warp 17         issues the MMAs: while one sub-tile's softmax runs, the
-//                   tensor cores work for the other
-//   warp 18         zeroes the rows of the last V tile that lie behind the
+//   warps 17, 18    one thread each issues the MMAs of sub-tile 0 / 1.  (Two,
+//                   because it takes a lone thread about 7 cycles per
+//                   instruction beside the softmax warps: one thread for
+//                   both sub-tiles needed 2 360 cycles a tile of 80 keys.)
+//   warp 19         zeroes the rows of the last V tile that lie behind the
 //                   document's end (a weight of 0 times whatever is there
 //                   must be 0)
 //
-// The tensor cores execute MMAs in the order they are issued, so S of tile
-// j + 1 may overwrite P of tile j right behind O += P V, and "S full" also
-// says that O holds every tile before.
+// S and P have columns of their own, so that S of the next tile is computed
+// while the softmax of this one runs, and the softmax warps never wait for a
+// product that waits for them.  With the O's of two sub-tiles in the 512
+// columns of tensor memory that leaves tiles of 128 keys at D = 64 and of 80
+// at D = 128.  (Tiles of 128 keys with P written over S, as D = 128 would
+// allow, took 3 250 cycles per 256 x 128 scores: the softmax of a sub-tile,
+// 1 950 cycles, and its two products, 1 250, one after the other.)
 //
-// What bounds it: a 128 x 128 tile costs 4 D * 128 * 128 operations of the
-// tensor cores (1024 cycles at D = 128, 512 at D = 64) and 128 * 128
-// exponentials of the special-function units (1024 cycles).
+// What bounds it, per 256 queries x 128 keys: the tensor cores, 4 D * 256 *
+// 128 operations (2048 cycles at D = 128; Q K^T reads its operands at the
+// limit of shared memory and takes 1.2 times its share), and the softmax:
+// 2048 cycles of the special-function units for the exponentials alone.
 #include <cuda.h>
 
 #include <cstring>
@@ -41,23 +48,23 @@ namespace {
 
 constexpr int kSub = 128;             // queries of a sub-tile
 constexpr int kTileQ = 2 * kSub;      // queries of a CTA
-constexpr int kTileK = 128;           // keys of a tile
+__host__ __device__ constexpr int tile_keys(int D) { return D == 128 ? 80 : 128; }
 constexpr int kSoftmaxWarps = 16;
 constexpr int kThreads = 32 * kSoftmaxWarps + 128;
 constexpr int kRegsSoftmax = 104;     // 512 * 104 + 128 * 64 = 640 * 96, the registers the CTA starts with
 constexpr int kRegsOther = 64;
-constexpr int kBlockBytes = 128 * 128;  // 128 rows x 64 values
-// A float per query and half of the keys (the softmax threads' exchange) and the barriers, in front of Q and the ring,
-// which are aligned to 1024 bytes: at D = 128 all of the 227 KB.
-constexpr int kExchange = 2 * 2 * kSub;
-constexpr int kHeadBytes = 3 * 1024;
-constexpr int kFma = 4;               // pairs of 16 whose exponentials run on the FMA units
 constexpr float kGrowth = 8.0f;       // log2 of the growth of a row's maximum that rescales O
 
-__host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * kBlockBytes; }
-__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 5 : 8; }
+// Blocks of 64 values (128 bytes) x rows: Q in sub-tiles of 128 rows, K and V in tiles of tile_keys rows.
+__host__ __device__ constexpr int q_bytes(int D) { return D / 64 * kSub * 128; }
+__host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * tile_keys(D) * 128; }
+__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 7 : 8; }
+// The softmax threads' exchange (two tiles' buffers of a float per half of the keys, sub-tile and query) and the
+// barriers, in front of Q and the ring, which are aligned to 1024 bytes.
+constexpr int kExchange = 2 * 2 * 2 * kSub;
+constexpr int kHeadBytes = 5 * 1024;
 __host__ __device__ constexpr int smem_bytes(int D) {
-  return kHeadBytes + (2 + ring_stages(D)) * tile_bytes(D);
+  return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D);
 }
 
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -102,28 +109,6 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   return r;
 }
 
-// 2^x of a pair on the FMA and integer units, for x in [-126, 127] (below:
-// 2^-126): x = n + f with n the nearest integer (read from the low bits of x +
-// 1.5 * 2^23) and |f| <= 1/2, 2^f by a polynomial of degree 5 (the minimax fit
-// of its relative error: 7.7e-8, 2.1e-7 as evaluated in binary32), and n added
-// to the exponent.
-__device__ __forceinline__ void ex2_pair_fma(uint64_t x, float& e0, float& e1) {
-  float x0, x1;
-  unpair(x, x0, x1);
-  x = pair(fmaxf(x0, -126.0f), fmaxf(x1, -126.0f));
-  const uint64_t shifted = add2(x, both(12582912.0f));
-  const uint64_t f = fma2(add2(shifted, both(-12582912.0f)), both(-1.0f), x);
-  uint64_t y = fma2(f, both(1.3277938903e-3f), both(9.6757576406e-3f));
-  y = fma2(y, f, both(5.5507095981e-2f));
-  y = fma2(y, f, both(2.4022114338e-1f));
-  y = fma2(y, f, both(6.9314696823e-1f));
-  y = fma2(y, f, both(1.0000000733f));
-  float n0, n1, y0, y1;
-  unpair(shifted, n0, n1);
-  unpair(y, y0, y1);
-  e0 = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(n0) << 23));
-  e1 = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(n1) << 23));
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -133,27 +118,36 @@ template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_tiles_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const AttnParams p, const int slots, int* err) {
+  constexpr int kTileK = tile_keys(D);
+  constexpr int kHalf = kTileK / 2;  // keys of a softmax thread
   constexpr int kStages = ring_stages(D);
+  constexpr int kQ = q_bytes(D);
   constexpr int kTile = tile_bytes(D);
   constexpr int kBlocks = D / 64;
+  constexpr int kQBlock = kSub * 128, kBlock = kTileK * 128;
   constexpr uint32_t kIdescS = make_idesc_bf16(kSub, kTileK, false);
   constexpr uint32_t kIdescO = make_idesc_bf16(kSub, D, true);
-  constexpr uint32_t kTmemCols = 512;  // S0, S1 (128 columns each), O0, O1 (D each)
+  // Columns of tensor memory: S and P of sub-tile s at s * kSpan, O behind them.
+  constexpr uint32_t kTmemCols = 512;
+  constexpr uint32_t kSpan = D == 128 ? 128 : 192;
+  constexpr uint32_t kColO = 2 * kSpan;
+  static_assert(kTileK + kTileK / 2 <= kSpan && kColO + 2 * D <= kTmemCols, "tensor memory");
 
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* exchange = reinterpret_cast<float*>(smem);  // [half][sub-tile][query]
+  float* exchange = reinterpret_cast<float*>(smem);  // [tile parity][half of the keys][sub-tile][query]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kExchange * sizeof(float));
-  uint8_t* sQ = smem + kHeadBytes;
-  uint8_t* ring = sQ + 2 * kTile;
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;   // [2]
-  uint64_t* s_full = q_full + 2;        // [2]
-  uint64_t* p_full = s_full + 2;        // [2]
-  uint64_t* o_full = p_full + 2;        // [2]
+  uint64_t* s_full = q_full + 2;        // [2] scores ready
+  uint64_t* s_free = s_full + 2;        // [2] scores read
+  uint64_t* p_full = s_free + 2;        // [2] weights ready
+  uint64_t* o_full = p_full + 2;        // [2] product with V done: O complete so far, P free
   uint64_t* tail_full = o_full + 2;
-  uint64_t* drain = tail_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* drain = tail_full + 1;      // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* sQ = smem + kHeadBytes;
+  uint8_t* ring = sQ + 2 * kQ;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // (known to be uniform)
   const int lane = threadIdx.x & 31;
@@ -186,16 +180,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both issuers
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&drain[s], 1);
       mbar_init(&q_full[s], 1);
       mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], kSoftmaxWarps / 2);
       mbar_init(&p_full[s], kSoftmaxWarps / 2);
       mbar_init(&o_full[s], 1);
     }
     mbar_init(tail_full, 1);
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -216,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftmaxWarps) {
     reg_lower<kRegsOther>();
     // One thread each: a warp that votes, elects and converges around every wait spends most of a tile's time on
-    // that (measured: 4 300 cycles a tile of 256 x 128 x 128, of which the issuing warp was idle in none).
+    // that.
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       return mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
     };
@@ -224,121 +219,123 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ loader
       const uint64_t keep = l2_policy_evict_last();
       const uint64_t once = l2_policy_evict_first();
-      int fills = 0;
+      // Fills in the order of their use: K of tile 0, then K of tile j + 1 and V of tile j.
+      int stage = 0, fills = 0;
+      uint32_t phase = 1;
+      bool ok = true;
       const auto load_q = [&](int s) {
-        mbar_arrive_expect_tx(&q_full[s], kTile);
+        mbar_arrive_expect_tx(&q_full[s], kQ);
         for (int b = 0; b < kBlocks; ++b) {
-          tma_load_3d_hint(sQ + s * kTile + b * kBlockBytes, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub, head,
-                           once);
+          tma_load_3d_hint(sQ + s * kQ + b * kQBlock, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub, head, once);
         }
       };
-      if (n0 > 0) load_q(0);
-      if (n1 > 0) load_q(1);
-      int stage = 0;
-      uint32_t phase = 1;
-      for (int f = 0; f < 2 * tiles; ++f) {
-        if (!wait(&empty[stage], phase, kSiteAttnLoad)) break;
-        // (a last V tile that ends inside goes to warp 18 first, which fills the slot)
-        uint64_t* landed = tail && f == 2 * tiles - 1 ? tail_full : &full[stage];
+      const auto load = [&](const CUtensorMap* map, int tile, uint64_t* landed) {
+        ok = wait(&empty[stage], phase, kSiteAttnLoad);
+        if (!ok) return;
+        if (landed == nullptr) landed = &full[stage];
         mbar_arrive_expect_tx(landed, kTile);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-          tma_load_3d_hint(ring + stage * kTile + b * kBlockBytes, (f & 1) ? &tm_v : &tm_k, landed, 64 * b,
-                           doc.k0 + (f >> 1) * kTileK, kv_head, keep);
+          tma_load_3d_hint(ring + stage * kTile + b * kBlock, map, landed, 64 * b, doc.k0 + tile * kTileK, kv_head,
+                           keep);
         }
         ++fills;
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1u;
         }
+      };
+      if (n0 > 0) load_q(0);
+      if (tiles > 0) load(&tm_k, 0, nullptr);
+      if (n1 > 0) load_q(1);
+      for (int j = 0; ok && j < tiles; ++j) {
+        if (j + 1 < tiles) load(&tm_k, j + 1, nullptr);
+        // (a last V tile that ends inside goes to warp 19 first, which fills the slot)
+        if (ok) load(&tm_v, j, tail && j + 1 == tiles ? tail_full : nullptr);
       }
       // Every load must have landed before the CTA ends (on the normal path they have).
       for (int f = max(0, fills - kStages); f < fills; ++f) {
         if (tail && f == 2 * tiles - 1) {
           mbar_wait_drain(tail_full, 0, p.timeout_ns, err);
-          continue;
+        } else {
+          mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
         }
-        mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
       }
       if (n0 > 0) mbar_wait_drain(&q_full[0], 0, p.timeout_ns, err);
       if (n1 > 0) mbar_wait_drain(&q_full[1], 0, p.timeout_ns, err);
-    } else if (warp == 17 && elect_one()) {
+    } else if ((warp == 17 || warp == 18) && elect_one()) {
       // -------------------------------------------------------- MMA issuer
+      const int s = warp - 17;
+      const int n = s == 0 ? n0 : n1;
       bool ok = true;
       // Matrix descriptors: the high words are constant, the low ones hold the address (in units of 16 bytes).
-      const uint64_t desc_k = make_smem_desc_k_sw128(0), desc_v = make_smem_desc_n_sw128(0, kBlockBytes);
-      const uint32_t q_addr = smem_u32(sQ) >> 4, ring_addr = smem_u32(ring) >> 4;
-      constexpr uint32_t kTile16 = kTile / 16, kBlock16 = kBlockBytes / 16;
-      // S_s = Q_s K^T with K in ring slot `stage`
-      const auto scores = [&](int s, int stage) {
-        const uint64_t qd = desc_k + (q_addr + s * kTile16), kd = desc_k + (ring_addr + stage * kTile16);
+      const uint64_t desc_q = make_smem_desc_k_sw128(smem_u32(sQ + s * kQ));
+      const uint64_t desc_k = make_smem_desc_k_sw128(smem_u32(ring)), desc_v = make_smem_desc_n_sw128(smem_u32(ring), kBlock);
+      const uint32_t t_s = tmem + s * kSpan, t_o = tmem + kColO + s * D;
+      int stage = 0;
+      uint32_t phase = 0;
+      const auto wait_fill = [&] { ok = wait(&full[stage], phase, kSiteAttnOperand); };
+      const auto release = [&] {  // the ring slot is free when the MMAs issued so far are done
+        mma_commit(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      const auto scores = [&] {  // S = Q K^T
+        const uint64_t kd = desc_k + stage * (kTile / 16);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          const uint32_t off = (x / 4) * kBlock16 + 2 * (x % 4);
-          mma_bf16_ss(tmem + s * kTileK, qd + off, kd + off, kIdescS, x > 0);
+          mma_bf16_ss(t_s, desc_q + ((x / 4) * (kQBlock / 16) + 2 * (x % 4)),
+                      kd + ((x / 4) * (kBlock / 16) + 2 * (x % 4)), kIdescS, x > 0);
         }
         mma_commit(&s_full[s]);
       };
-      if (tiles > 0) ok = wait(&full[0], 0, kSiteAttnOperand);
-#pragma unroll 1
-      for (int s = 0; ok && s < 2; ++s) {
-        if ((s == 0 ? n0 : n1) == 0) continue;
-        ok = wait(&q_full[s], 0, kSiteAttnOperand);
-        if (ok) scores(s, 0);
-      }
-      if (ok && tiles > 0) mma_commit(&empty[0]);
-      int v_stage = 1;
-      uint32_t v_phase = 0;
-      for (int j = 0; ok && j < tiles; ++j) {
-        int k_stage = v_stage + 1;  // of tile j + 1
-        uint32_t k_phase = v_phase;
-        if (k_stage == kStages) {
-          k_stage = 0;
-          k_phase ^= 1u;
+      if (tiles > 0) {
+        wait_fill();
+        if (ok && n > 0) {
+          ok = wait(&q_full[s], 0, kSiteAttnOperand);
+          if (ok) scores();
         }
-        ok = wait(&full[v_stage], v_phase, kSiteAttnOperand) &&
-             (j + 1 == tiles || wait(&full[k_stage], k_phase, kSiteAttnOperand));
-        if (!ok) break;
-#pragma unroll 1
-        for (int s = 0; s < 2; ++s) {
-          const int n = s == 0 ? n0 : n1;
-          if (j >= n) continue;
-          ok = wait(&p_full[s], static_cast<uint32_t>(j & 1), kSiteAttnWeights);
+        if (ok) release();
+      }
+      for (int j = 0; ok && j < tiles; ++j) {
+        const uint32_t parity = static_cast<uint32_t>(j & 1);
+        if (j + 1 < tiles) {
+          wait_fill();
+          if (ok && j + 1 < n) {
+            ok = wait(&s_free[s], parity, kSiteAttnWeights);
+            tc_fence_after_sync();
+            if (ok) scores();
+          }
+          if (!ok) break;
+          release();
+        }
+        wait_fill();
+        if (ok && j < n) {
+          ok = wait(&p_full[s], parity, kSiteAttnWeights);
           if (!ok) break;
           tc_fence_after_sync();
-          const uint64_t vd = desc_v + (ring_addr + v_stage * kTile16);
+          const uint64_t vd = desc_v + stage * (kTile / 16);
 #pragma unroll
           for (int x = 0; x < kTileK / 16; ++x) {
-            mma_bf16_ts(tmem + 2 * kTileK + s * D, tmem + s * kTileK + 8 * x, vd + 128 * x, kIdescO,
-                        (x > 0 || j > 0) ? 1u : 0u);
+            mma_bf16_ts(t_o, t_s + kTileK + 8 * x, vd + 128 * x, kIdescO, (x > 0 || j > 0) ? 1u : 0u);
           }
-          if (j + 1 < n) {
-            scores(s, k_stage);
-          } else {
-            mma_commit(&o_full[s]);
-          }
+          mma_commit(&o_full[s]);
         }
-        if (!ok) break;
-        mma_commit(&empty[v_stage]);
-        if (j + 1 < tiles) mma_commit(&empty[k_stage]);
-        v_stage = k_stage + 1;
-        v_phase = k_phase;
-        if (v_stage == kStages) {
-          v_stage = 0;
-          v_phase ^= 1u;
-        }
+        if (ok) release();
       }
       // No MMA may still run when tensor memory is freed.
-      mma_commit(drain);
-      mbar_wait_drain(drain, 0, p.timeout_ns, err);
-    } else if (warp == 18 && tail) {
+      mma_commit(&drain[s]);
+      mbar_wait_drain(&drain[s], 0, p.timeout_ns, err);
+    } else if (warp == 19 && tail) {
       // ------------------------------------------------ end of the document
       const int stage = (2 * tiles - 1) % kStages;
       if (warp_wait(tail_full, 0, abort_flag, p.timeout_ns, err, kSiteAttnOperand)) {
         uint8_t* v = ring + stage * kTile;
         for (int x = tail_rows * 8 + lane; x < kTileK * 8; x += 32) {
 #pragma unroll
-          for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4*>(v + b * kBlockBytes + x * 16) = make_uint4(0, 0, 0, 0);
+          for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4*>(v + b * kBlock + x * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
       }
@@ -350,14 +347,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- softmax
     reg_raise<kRegsSoftmax>();
     const int s = warp >> 3;
-    const int part = (warp >> 2) & 1;  // keys 64 part .. 64 part + 63 of every tile
+    const int part = (warp >> 2) & 1;  // keys kHalf * part .. of every tile
     const int quarter = warp & 3;
     const uint32_t partners = 1 + (warp >> 3) * 4 + quarter;  // named barrier of the two warps of 32 queries
     const int my_rows = min(kSub, rows - s * kSub);  // <= 0: nothing in this sub-tile
     const int n = s == 0 ? n0 : n1;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lanes + s * kTileK;
-    const uint32_t t_o = tmem + lanes + 2 * kTileK + s * D;
+    const uint32_t t_s = tmem + lanes + s * kSpan + kHalf * part;
+    const uint32_t t_p = tmem + lanes + s * kSpan + kTileK + kHalf / 2 * part;
+    const uint32_t t_o = tmem + lanes + kColO + s * D + D / 2 * part;
     const int in_sub = quarter * 32 + lane;
     const int i = row0 + s * kSub + in_sub;  // the thread's query
     const int limit = in_sub < my_rows ? max(0, key_limit(p, doc, i)) : 0;
@@ -371,17 +369,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int place = i + doc.shift;
     const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
 
-    // 32 scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
-    auto first_pass = [&](uint32_t (&v)[32], int key0, bool masked) {
+    // Scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
+    const auto first_pass = [&](auto& v, int key0, bool masked) {
+      constexpr int N = sizeof(v) / sizeof(v[0]);
       if constexpr (CAP) {
         // Scores within the cap on either side (all of them, unless the scores are far beyond it) take the
         // polynomial for tanh; others two special functions each.
         float far = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 32; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
+        for (int x = 0; x < N; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
         if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
+          for (int x = 0; x < N; x += 2) {
             const uint64_t y = mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), both(inv_cap));
             const uint64_t u = mul2(y, y);
             uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
@@ -396,22 +395,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
+          for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
         }
       }
       if constexpr (BIAS) {
         const float f = CAP ? 1.0f : c;
         const float first = static_cast<float>(key0 - place);  // distance of the first key, signed
-        if (key0 + 31 <= first_place) {
+        if (key0 + N - 1 <= first_place) {
           // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
           const float at0 = slope * first;
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < N; ++x) {
             v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, fmaf(slope, static_cast<float>(x), at0)));
           }
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < N; ++x) {
             v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, -slope * fabsf(first + static_cast<float>(x))));
           }
         }
@@ -419,49 +418,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (masked) {
         const int left = limit - key0;
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
+        for (int x = 0; x < N; ++x) {
           if (x >= left) v[x] = 0xFF800000u;  // -inf
         }
       }
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < 32; x += 4) {
+      for (int x = 0; x < N; x += 4) {
         top[0] = max3(top[0], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
         top[1] = max3(top[1], __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
       }
       return fmax_nan(top[0], top[1]);
     };
 
-    // The value of the thread with the other 64 keys of this query.  One barrier is enough: a thread writes its
-    // next value when the MMAs that wait for its partner's weights are done, so after the partner read this one.
-    float* const mine = exchange + (part * 2 + s) * kSub + in_sub;
-    const float* const other = exchange + ((part ^ 1) * 2 + s) * kSub + in_sub;
-    const auto partner = [&](float x) {
-      *mine = x;
+    // The value of the thread with the other half of this query's keys.  One barrier is enough with two buffers in
+    // turn: a buffer is written again behind the next tile's barrier, where the partner has read it.  (A warp that
+    // aborts arrives once more, and its partner looks at the flag before it comes back, so that none is left waiting.)
+    const auto partner = [&](float x, int turn) {
+      float* const at = exchange + (turn & 1) * (4 * kSub) + s * kSub + in_sub;
+      at[part * 2 * kSub] = x;
       named_barrier_sync(partners, 64);
-      return *other;
+      return at[(part ^ 1) * 2 * kSub];
+    };
+    const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+      const bool done = mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
+      return __all_sync(0xFFFFFFFFu, done && !*abort_flag);
     };
 
     float m = -INFINITY;  // in units of log2
     float l = 0.0f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = warp_wait(&s_full[s], static_cast<uint32_t>(j & 1), abort_flag, p.timeout_ns, err, kSiteAttnScores);
+      ok = wait(&s_full[s], static_cast<uint32_t>(j & 1), kSiteAttnScores);
       if (!ok) break;
       tc_fence_after_sync();
       const bool masked = (j + 1) * kTileK > least;
-      const int key0 = j * kTileK + 64 * part;
-      uint32_t va[32], vb[32];
-      tmem_load_32cols_async(t_s + 64 * part, va);
-      tmem_load_32cols_async(t_s + 64 * part + 32, vb);
-      tmem_wait_load(va);
-      tmem_wait_load(vb);
-      float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
-      // The partner's maximum.  (Behind the barrier both have read their scores, and P may be written over them.)
+      const int key0 = j * kTileK + kHalf * part;
+      uint32_t va[32], vb[kHalf - 32];
+      tmem_load_cols_async(t_s, va);
+      tmem_load_cols_async(t_s + 32, vb);
+      tmem_wait_loads(va);
+      tmem_wait_loads(vb);
       tc_fence_before_sync();
-      top = fmax_nan(top, partner(top));
-      tc_fence_after_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[s]);
+      float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
+      top = fmax_nan(top, partner(top, j));
       if (!kChange) top *= c;  // c > 0
+      // P and O are free when the last tile's product is done.  (To wait here, rather than behind the exponentials,
+      // keeps the two sub-tiles out of step: 427 us against 448 for 2 x 4608 tokens, 24 heads of 128.  When both
+      // compute exponentials at the same time, both come to wait at the same time.)
+      if (j > 0) {
+        ok = wait(&o_full[s], static_cast<uint32_t>(j - 1) & 1u, kSiteAttnOut);
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
       if (j == 0) {
         m = top;
       } else {
@@ -473,44 +484,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int b = 0; b < D / 32; ++b) {
             uint32_t o[16];
-            tmem_load_16cols(t_o + D / 2 * part + 16 * b, o);
+            tmem_load_16cols(t_o + 16 * b, o);
 #pragma unroll
             for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_store_16cols(t_o + D / 2 * part + 16 * b, o);
+            tmem_store_cols(t_o + 16 * b, o);
           }
         }
       }
       const float base = m == -INFINITY ? 0.0f : m;
       const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
       uint64_t sums[2] = {both(0.0f), both(0.0f)};
-      // Weights of 32 keys.  In whole tiles kFma of every 16 pairs take their exponentials on the FMA units; masked
-      // tiles need 2^-inf = 0.
-      auto weights = [&](const uint32_t (&v)[32], int b, bool mixed) {
-        uint32_t w[16];
+      // Weights of 2 N keys.  (A part of the exponentials as polynomials on the FMA units, to relieve the special-function
+      // units, made it slower: 438 us against 427 with an eighth of them, 453 with three eighths, at 2 x 4608 tokens, 24
+      // heads of 128.  Two warps per scheduler do not hide the polynomial's latency.)
+      const auto weights = [&](const uint32_t* v, auto& w) {
+        constexpr int N = sizeof(w) / sizeof(w[0]);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
+        for (int x = 0; x < N; ++x) {
           const uint64_t y = pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
           const uint64_t e = kChange ? add2(y, minus) : fma2(y, c2, minus);
           float a0, a1;
-          if (mixed && x * kFma / 16 != (x + 1) * kFma / 16) {
-            ex2_pair_fma(e, a0, a1);
-          } else {
-            unpair(e, a0, a1);
-            a0 = ex2(a0);
-            a1 = ex2(a1);
-          }
+          unpair(e, a0, a1);
+          a0 = ex2(a0);
+          a1 = ex2(a1);
           sums[x & 1] = add2(sums[x & 1], pair(a0, a1));
           w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
         }
-        tmem_store_16cols(t_s + 32 * part + 16 * b, w);
       };
-      if (kFma == 0 || masked) {
-        weights(va, 0, false);
-        weights(vb, 1, false);
-      } else {
-        weights(va, 0, true);
-        weights(vb, 1, true);
-      }
+      uint32_t wa[16], wb[kHalf / 2 - 16];
+      weights(va, wa);
+      weights(vb, wb);
+      tmem_store_cols(t_p, wa);
+      tmem_store_cols(t_p + 16, wb);
       tmem_wait_store();
       tc_fence_before_sync();
       __syncwarp();
@@ -521,22 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     // ------------------------------------------------------------- epilogue
-    if (ok && n > 0) ok = warp_wait(&o_full[s], 0, abort_flag, p.timeout_ns, err, kSiteAttnOut);
+    if (ok && n > 0) ok = wait(&o_full[s], static_cast<uint32_t>(n - 1) & 1u, kSiteAttnOut);
     if (!ok) named_barrier_arrive(partners, 64);  // the partner may stand at its barrier: it will see the abort next
     if (ok && my_rows > 0) {
       tc_fence_after_sync();
-      l += partner(l);
+      l += partner(l, n);
       const bool any = limit > 0;
       const float inv = any ? 1.0f / l : 0.0f;
       // The warp's 32 rows x D/2 values through shared memory (its part of the sub-tile's Q, which no MMA reads any
       // more), so that they leave in whole segments of D bytes.
       constexpr int kVec = D / 16;  // 16-byte vectors of a row
-      uint8_t* stage = sQ + s * kTile + (part * 4 + quarter) * 32 * D;
+      uint8_t* stage = sQ + s * kQ + (part * 4 + quarter) * 32 * D;
 #pragma unroll 1
       for (int b = 0; b < D / 32; ++b) {
         uint32_t o[16];
         if (n > 0) {
-          tmem_load_16cols(t_o + D / 2 * part + 16 * b, o);
+          tmem_load_16cols(t_o + 16 * b, o);
         } else {
 #pragma unroll
           for (int x = 0; x < 16; ++x) o[x] = 0u;
@@ -587,8 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// {64 values, tokens, heads} boxes of 64 x 128 x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
-bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs) {
+// {64 values, tokens, heads} boxes of 64 x box_rows x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
+bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs,
+                  int box_rows) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),
@@ -596,7 +602,7 @@ bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int
   // (the stride of a dimension of one is free)
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (tokens > 1 ? ld : D)),
                                  static_cast<cuuint64_t>(2 * (heads > 1 ? hs : D))};
-  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -609,11 +615,11 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   std::memset(&tm_q, 0, sizeof tm_q);
   // No keys: no tile of them is ever loaded, and the maps describe q.
   const bool none = p.tokens_k == 0;
-  bool ok = encode_heads(&tm_q, p.q, D, p.tokens_q, p.heads_q, p.ldq, p.hsq);
+  bool ok = encode_heads(&tm_q, p.q, D, p.tokens_q, p.heads_q, p.ldq, p.hsq, kSub);
   tm_k = tm_v = tm_q;
   if (!none) {
-    ok = ok && encode_heads(&tm_k, p.k, D, p.tokens_k, p.heads_k, p.ldk, p.hsk) &&
-         encode_heads(&tm_v, p.v, D, p.tokens_k, p.heads_k, p.ldv, p.hsv);
+    ok = ok && encode_heads(&tm_k, p.k, D, p.tokens_k, p.heads_k, p.ldk, p.hsk, tile_keys(D)) &&
+         encode_heads(&tm_v, p.v, D, p.tokens_k, p.heads_k, p.ldv, p.hsv, tile_keys(D));
   }
   if (!ok) return cudaErrorInvalidValue;
   int* err = nullptr;
@@ -621,7 +627,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
-  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 10) * 8 + 8 <= kHeadBytes, "shared memory");
+  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 13) * 8 + 8 <= kHeadBytes, "shared memory");
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int64_t slots = p.tokens_q / kTileQ + p.docs;
