@@ -107,3 +107,12 @@ def test_attention(w8, change, status):
 
 def test_attention_needs_arguments(w8):
     assert w8.raw_lib().w8a8_attention(None, None) == 1
+
+
+def test_packed_descriptors_have_the_structures_layout(w8):
+    assert w8._QK_DESC.size == ctypes.sizeof(w8.QkDesc)
+    assert w8._ATTENTION_DESC.size == ctypes.sizeof(w8.AttentionDesc)
+    for layout, desc in ((w8._QK_DESC, w8.QkDesc), (w8._ATTENTION_DESC, w8.AttentionDesc)):
+        values = list(range(1, 1 + len(desc._fields_)))
+        d = desc.from_buffer_copy(layout.pack(*values))
+        assert [getattr(d, name) for name, _ in desc._fields_] == values

@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -86,6 +87,12 @@ class QkDesc(ctypes.Structure):
                 + [("eps", ctypes.c_float)])
 
 
+# The descriptors' layouts for struct, which packs one in a quarter of the time that it takes to fill a ctypes
+# structure (a null pointer is 0).
+_QK_DESC = struct.Struct("@9P10q5if0q")
+_ATTENTION_DESC = struct.Struct("@9P10q5i2f0q")
+
+
 class AttentionDesc(ctypes.Structure):
     """w8a8_attention_desc: the arguments of w8a8_attention."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "cu_q", "cu_k", "prefix", "slopes")]
@@ -132,8 +139,8 @@ def _load() -> ctypes.CDLL:
                                  ctypes.c_int),
         "w8a8_linear_glu": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
         "w8a8_linear_glu_fp8": ([p, p, p, p, p, p, p, i64, i64, i64, i32, p], ctypes.c_int),
-        "w8a8_qk_norm_rope": ([ctypes.POINTER(QkDesc), p], ctypes.c_int),
-        "w8a8_attention": ([ctypes.POINTER(AttentionDesc), p], ctypes.c_int),
+        "w8a8_qk_norm_rope": ([p, p], ctypes.c_int),  # a QkDesc, or its packed bytes
+        "w8a8_attention": ([p, p], ctypes.c_int),
         "w8a8_chain_create": ([ctypes.POINTER(LinearDesc), i32, ctypes.POINTER(p)], ctypes.c_int),
         "w8a8_chain_launch": ([p, p], ctypes.c_int),
         "w8a8_chain_layers": ([p], i32),
@@ -170,6 +177,8 @@ def _check(status: int, what: str) -> None:
 
 def _stream(stream, device) -> int | None:
     if stream is None:
+        if device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -194,6 +203,9 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype, ndim: int) -> None:
 
 
 def _need_contig(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> None:
+    # A tensor as it should be passes on the first line (a call's checks would otherwise outlast a short kernel).
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
     _need(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -591,15 +603,15 @@ def _gemm_glu(fn, what, code, xq, wq, scale_a, scale_w, bias, out, act, config, 
     _need_contig(out, "out", torch.bfloat16, (M, N))
     dev = _one_device(xq, wq, scale_a, scale_w, bias, out)
     c = _cfg(config)
-    with torch.cuda.device(dev):
-        _check(fn(_ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K, int(act),
-                  ctypes.byref(c) if c is not None else None, _stream(stream, dev)), what)
+    _check(_call(dev, fn, _ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K, int(act),
+                 ctypes.byref(c) if c is not None else None, _stream(stream, dev)), what)
     return out
 
 
 def _glu_weight(wq, code, K, scale_w, bias) -> int:
     """Checks the weight of a gated layer, [2N, K] with its scales and bias; N."""
-    _need(wq, "wq", code, 2)
+    if not (isinstance(wq, torch.Tensor) and len(wq.shape) == 2):
+        _need(wq, "wq", code, 2)
     if wq.shape[0] % 2:
         raise ValueError(f"wq must have an even number of rows (gate, then up), got {wq.shape[0]}")
     if wq.shape[1] != K:
@@ -637,23 +649,26 @@ def w8a8_gemm_glu_fp8(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = 
 
 
 def _linear_glu(fn, what, code, x, wq, scale_w, bias, out, act, ws_xq, ws_scale_a, stream):
-    _need(x, "x", torch.bfloat16, 2)
+    if not (isinstance(x, torch.Tensor) and len(x.shape) == 2):
+        _need(x, "x", torch.bfloat16, 2)
     M, K = x.shape
     _need_contig(x, "x", torch.bfloat16, (M, K))
     N = _glu_weight(wq, code, K, scale_w, bias)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need_contig(out, "out", torch.bfloat16, (M, N))
     if ws_xq is None:
         ws_xq = torch.empty((M, K), dtype=code, device=x.device)
+    else:
+        _need_contig(ws_xq, "ws_xq", code, (M, K))
     if ws_scale_a is None:
         ws_scale_a = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _need_contig(out, "out", torch.bfloat16, (M, N))
-    _need_contig(ws_xq, "ws_xq", code, (M, K))
-    _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
+    else:
+        _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
     dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
-    with torch.cuda.device(dev):
-        _check(fn(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq), _ptr(ws_scale_a), M, N, K,
-                  int(act), _stream(stream, dev)), what)
+    _check(_call(dev, fn, _ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq), _ptr(ws_scale_a), M, N,
+                 K, int(act), _stream(stream, dev)), what)
     return out
 
 
@@ -677,20 +692,45 @@ def w8a8_linear_glu_fp8(x, wq, scale_w, bias=None, out=None, act: int = ACT_SILU
 
 def _heads(t: torch.Tensor, name: str, dim: int | None = None) -> tuple:
     """Checks a bf16 [tokens, heads, head_dim] tensor; its (token, head) strides in elements."""
-    _need(t, name, torch.bfloat16, 3)
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and len(t.shape) == 3):
+        _need(t, name, torch.bfloat16, 3)
     rows, heads, d = t.shape
+    ld, hs, one = t.stride()
+    if one != 1 and t.numel() > 0:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
     if dim is not None and d != dim:
         raise ValueError(f"{name} must have head dimension {dim}, got {d}")
-    hs = t.stride(1) if heads > 1 else d
-    return (t.stride(0) if rows > 1 else max(1, heads) * hs), hs
+    if heads <= 1:
+        hs = d
+    return (ld if rows > 1 else max(1, heads) * hs), hs
+
+
+def _heads_out(t, name: str, like: torch.Tensor) -> tuple:
+    """An output of the shape of `like`, allocated (contiguous) if t is None, and its strides."""
+    if t is None:
+        rows, heads, d = like.shape
+        return torch.empty((rows, heads, d), dtype=torch.bfloat16, device=like.device), max(1, heads) * d, d
+    strides = _heads(t, name, like.shape[2])
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return t, *strides
 
 
 def _one_device(*tensors) -> torch.device:
-    """The device the given tensors (None skipped) share."""
-    dev = [t.device for t in tensors if t is not None]
-    if any(d != dev[0] for d in dev):
-        raise ValueError(f"tensors are on different devices: {sorted({str(d) for d in dev})}")
-    return dev[0]
+    """The device the given tensors (None skipped; the first is not None) share."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors are on different devices: {sorted({str(t.device) for t in tensors if t is not None})}")
+    return tensors[0].device
+
+
+def _call(dev: torch.device, fn, *args) -> int:
+    """fn(*args) with dev as the current device (entered only if another one is)."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps: float = 1e-6,
@@ -717,20 +757,13 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
         _need_contig(sin, "sin", torch.float32, (rows, rot // 2))
     if positions is not None:
         _need_contig(positions, "positions", torch.int32, (M,))
-    if q_out is None:
-        q_out = torch.empty((M, hq, D), dtype=torch.bfloat16, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(tuple(k.shape), dtype=torch.bfloat16, device=q.device)
-    ldqo, hsqo = _heads(q_out, "q_out", D)
-    ldko, hsko = _heads(k_out, "k_out", D)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("outputs must have the shapes of q and k")
+    q_out, ldqo, hsqo = _heads_out(q_out, "q_out", q)
+    k_out, ldko, hsko = _heads_out(k_out, "k_out", k)
     dev = _one_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
-    desc = QkDesc(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                  _ptr(positions), M, rows, ldq, hsq, ldk, hsk, ldqo, hsqo, ldko, hsko, hq, k.shape[1], D, rot,
-                  int(layout), float(eps))
-    with torch.cuda.device(dev):
-        _check(_lib.w8a8_qk_norm_rope(ctypes.byref(desc), _stream(stream, dev)), "w8a8_qk_norm_rope")
+    desc = _QK_DESC.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight) or 0,
+                         _ptr(k_weight) or 0, _ptr(cos) or 0, _ptr(sin) or 0, _ptr(positions) or 0, M, rows, ldq, hsq,
+                         ldk, hsk, ldqo, hsqo, ldko, hsko, hq, k.shape[1], D, rot, int(layout), float(eps))
+    _check(_call(dev, _lib.w8a8_qk_norm_rope, desc, _stream(stream, dev)), "w8a8_qk_norm_rope")
     return q_out, k_out
 
 
@@ -749,30 +782,28 @@ def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal
     ldk, hsk = _heads(k, "k", D)
     ldv, hsv = _heads(v, "v", D)
     Tk, Hk = k.shape[:2]
-    if tuple(v.shape) != tuple(k.shape):
+    if v.shape != k.shape:
         raise ValueError(f"v must have the shape of k, got {tuple(v.shape)} and {tuple(k.shape)}")
-    for c, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        if c is not None:
-            _need(c, name, torch.int32, 1)
-            docs = c.shape[0] - 1 if docs is None else docs
-    docs = 1 if docs is None else int(docs)
-    for c, name, n, kind in ((cu_q, "cu_q", docs + 1, torch.int32), (cu_k, "cu_k", docs + 1, torch.int32),
-                             (prefix, "prefix", docs, torch.int32), (slopes, "slopes", Hq, torch.float32)):
-        if c is not None:
-            _need_contig(c, name, kind, (n,))
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=torch.bfloat16, device=q.device)
-    ldo, hso = _heads(out, "out", D)
-    if out.shape != q.shape:
-        raise ValueError(f"out must have the shape of q, got {tuple(out.shape)}")
+    if docs is None:
+        starts = cu_q if cu_q is not None else cu_k
+        docs = 1 if starts is None else starts.shape[0] - 1
+    if cu_q is not None:
+        _need_contig(cu_q, "cu_q", torch.int32, (docs + 1,))
+    if cu_k is not None:
+        _need_contig(cu_k, "cu_k", torch.int32, (docs + 1,))
+    if prefix is not None:
+        _need_contig(prefix, "prefix", torch.int32, (docs,))
+    if slopes is not None:
+        _need_contig(slopes, "slopes", torch.float32, (Hq,))
+    out, ldo, hso = _heads_out(out, "out", q)
     if lse is not None:
         _need_contig(lse, "lse", torch.float32, (Tq, Hq))
     dev = _one_device(q, k, v, cu_q, cu_k, prefix, slopes, out, lse)
-    desc = AttentionDesc(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_q), _ptr(cu_k), _ptr(prefix),
-                         _ptr(slopes), Tq, Tk, ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D,
-                         1 if causal else 0, float(D ** -0.5 if scale is None else scale), float(cap))
-    with torch.cuda.device(dev):
-        _check(_lib.w8a8_attention(ctypes.byref(desc), _stream(stream, dev)), "w8a8_attention")
+    desc = _ATTENTION_DESC.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse) or 0,
+                                _ptr(cu_q) or 0, _ptr(cu_k) or 0, _ptr(prefix) or 0, _ptr(slopes) or 0, Tq, Tk, ldq,
+                                hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D, 1 if causal else 0,
+                                float(D ** -0.5 if scale is None else scale), float(cap))
+    _check(_call(dev, _lib.w8a8_attention, desc, _stream(stream, dev)), "w8a8_attention")
     return out
 
 

@@ -2,10 +2,13 @@
 // packed documents, the masks as one limit per query, and the scores.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
+
+#include "internal.h"
 
 namespace w8a8 {
 
@@ -26,6 +29,23 @@ struct AttnParams {
   float scale, cap;
   uint64_t timeout_ns;
 };
+
+// {64 values, tokens, heads} boxes of 64 x box_rows x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
+inline bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs,
+                  int box_rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),
+                              static_cast<cuuint64_t>(heads)};
+  // (the stride of a dimension of one is free)
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (tokens > 1 ? ld : D)),
+                                 static_cast<cuuint64_t>(2 * (heads > 1 ? hs : D))};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_attention_rows(const AttnParams& p, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, cudaStream_t stream);

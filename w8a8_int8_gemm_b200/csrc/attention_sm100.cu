@@ -592,23 +592,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// {64 values, tokens, heads} boxes of 64 x box_rows x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
-bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs,
-                  int box_rows) {
-  EncodeTiledFn fn = get_encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),
-                              static_cast<cuuint64_t>(heads)};
-  // (the stride of a dimension of one is free)
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (tokens > 1 ? ld : D)),
-                                 static_cast<cuuint64_t>(2 * (heads > 1 ? hs : D))};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool CAP, bool BIAS>
 cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -628,7 +611,8 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
   static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 13) * 8 + 8 <= kHeadBytes, "shared memory");
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> set{0};
+  e = allow_shared_memory(kernel, smem, set);
   if (e != cudaSuccess) return e;
   const int64_t slots = p.tokens_q / kTileQ + p.docs;
   if (slots * p.heads_q > 2147483647) return cudaErrorInvalidValue;

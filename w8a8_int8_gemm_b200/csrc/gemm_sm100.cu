@@ -897,7 +897,8 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
 
   const int smem = smem_bytes(PAIR, BN, p.stages * KCH);
   auto kernel = gemm_w8a8_kernel<BN, OUT, PAIR, FUSE, EL, KCH>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> set{0};
+  e = allow_shared_memory(kernel, kSmemLimit, set);
   if (e != cudaSuccess) return e;
   // Persistent grid: one CTA (or CTA pair) per tile at most.
   int units = (PAIR ? cfg.grid / 2 : cfg.grid);

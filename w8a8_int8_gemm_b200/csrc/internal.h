@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/w8a8.h"
@@ -117,6 +118,19 @@ inline w8a8_status status_of(cudaError_t e) {
   if (e == cudaSuccess) return W8A8_OK;
   if (e == cudaErrorInvalidValue) return W8A8_ERR_INVALID_ARG;
   return W8A8_ERR_LAUNCH;
+}
+// Lets a kernel use `bytes` of dynamic shared memory; set once per device and kernel (mask: the kernel's own).
+template <class Kernel>
+cudaError_t allow_shared_memory(Kernel kernel, int bytes, std::atomic<uint64_t>& mask) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const uint64_t bit = uint64_t{1} << dev;
+  if (mask.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) mask.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 bool rows_disjoint(int64_t rows, int64_t ld, int64_t heads, int64_t hs, int64_t dim);
 

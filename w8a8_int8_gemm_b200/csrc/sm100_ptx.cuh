@@ -520,6 +520,15 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* map, uin
       : "memory");
 }
 
+// The same without a policy.
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Registers per thread of this warpgroup (a multiple of 8; all its warps execute it).
 template <int N>
 __device__ __forceinline__ void reg_raise() {
