@@ -67,31 +67,6 @@ __host__ __device__ constexpr int smem_bytes(int D) {
   return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D);
 }
 
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t both(float a) { return pair(a, a); }
-
 // tanh(y) = y * sum_n kTanh[n] y^2n on [-1, 1]: least squares on Chebyshev nodes, relative error 7e-7 in binary32.
 __device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
                                        -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};

@@ -16,7 +16,10 @@
 // in two lanes of the same head (halves: one shuffle per value).  A warp
 // holds 32/L heads at a time and kSteps times that many of one token in all,
 // loaded together so that 64 bytes per lane are in flight, and reads the
-// token's table row once for them.
+// token's table row and the weights once for them.  The arithmetic is on
+// pairs of binary32: one value at a time, with q and k mixed in a warp, the
+// instructions alone took as long as the memory (51 us for 9216 tokens of 48
+// heads of 128).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,12 +27,14 @@
 
 #include "../../include/w8a8.h"
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace w8a8 {
 namespace {
 
 constexpr int kSteps = 4;
 constexpr int kWarps = 8;
+constexpr int kBlocksPerSm = 4;
 
 struct QkParams {
   const __nv_bfloat16* x[2];  // q, k
@@ -42,24 +47,24 @@ struct QkParams {
   int64_t M, table_rows;
   int heads[2];
   int D, R;
-  int units;  // warps per token
+  int units, units_q;  // warps per token, and those of q among them
   float eps, inv_d;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+// Eight bf16 values as four pairs of binary32, and back (one rounding).
+__device__ __forceinline__ void unpack8(const uint4& v, uint64_t (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    float a, b;
+    unpair(f[i], a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -67,7 +72,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 // L: lanes per head (2 .. 32).  PAIRS: the rotation's pairing.
 template <int L, bool PAIRS>
-__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) qk_norm_rope_kernel(const QkParams p) {
   constexpr int kPerStep = 32 / L;            // heads of one step
   constexpr int kTable = PAIRS ? 4 : 8;       // table entries of a lane
   const int lane = threadIdx.x & 31;
@@ -79,89 +84,97 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const QkParam
   const bool upper = !PAIRS && sub >= half_lanes;  // holds the b of its pairs
   const int mate = grp * L + (upper ? sub - half_lanes : sub + half_lanes);
   const int entry = PAIRS ? 4 * sub : 8 * (upper ? sub - half_lanes : sub);
-  const int all_heads = p.heads[0] + p.heads[1];
-
-  uint4 wv[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    wv[j] = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);  // ones
-    if (p.w[j] != nullptr && in_head) wv[j] = __ldg(reinterpret_cast<const uint4*>(p.w[j] + 8 * sub));
-  }
-
   const int64_t total = p.M * p.units;
   for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); unit < total;
        unit += static_cast<int64_t>(gridDim.x) * kWarps) {
-    const int64_t m = unit / p.units;
-    const int head0 = static_cast<int>(unit - m * p.units) * (kSteps * kPerStep) + grp;
+    // (a 64-bit division only where the number of units needs it)
+    const int64_t m = total <= 0x7FFFFFFF ? static_cast<int>(unit) / p.units : unit / p.units;
+    int u = static_cast<int>(unit - m * p.units);
+    const int j = u >= p.units_q;  // this unit's heads are of q or of k
+    if (j) u -= p.units_q;
+    const int head0 = u * (kSteps * kPerStep) + grp;
+    const int heads = p.heads[j];
+    const __nv_bfloat16* x = p.x[j] + m * p.ld[j] + 8 * sub;
+    __nv_bfloat16* y = p.y[j] + m * p.ld_y[j] + 8 * sub;
 
     uint4 v[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int h = head0 + s * kPerStep;
       v[s] = make_uint4(0, 0, 0, 0);
-      if (h < all_heads && in_head) {
-        const int j = h >= p.heads[0];
-        const int hj = j ? h - p.heads[0] : h;
-        v[s] = *reinterpret_cast<const uint4*>(p.x[j] + m * p.ld[j] + hj * p.hs[j] + 8 * sub);
-      }
+      if (h < heads && in_head) v[s] = *reinterpret_cast<const uint4*>(x + h * p.hs[j]);
     }
 
-    float c[kTable], sn[kTable];
+    uint64_t c[kTable / 2], sn[kTable / 2];  // pairs of binary32
     if (p.cos != nullptr) {
       const int64_t row = p.positions != nullptr ? static_cast<int64_t>(__ldg(p.positions + m)) : m;
       // A position outside the table reads nothing and turns by NaN.
       const bool known = row >= 0 && row < p.table_rows;
 #pragma unroll
-      for (int i = 0; i < kTable; ++i) c[i] = sn[i] = __int_as_float(0x7FFFFFFF);
+      for (int i = 0; i < kTable / 2; ++i) c[i] = sn[i] = both(__int_as_float(0x7FFFFFFF));
       if (turns && known) {
-        const float4* cr = reinterpret_cast<const float4*>(p.cos + row * (p.R / 2) + entry);
-        const float4* sr = reinterpret_cast<const float4*>(p.sin + row * (p.R / 2) + entry);
+        const ulonglong2* cr = reinterpret_cast<const ulonglong2*>(p.cos + row * (p.R / 2) + entry);
+        const ulonglong2* sr = reinterpret_cast<const ulonglong2*>(p.sin + row * (p.R / 2) + entry);
 #pragma unroll
         for (int i = 0; i < kTable / 4; ++i) {
-          const float4 a = __ldg(cr + i), b = __ldg(sr + i);
-          c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
-          sn[4 * i] = b.x, sn[4 * i + 1] = b.y, sn[4 * i + 2] = b.z, sn[4 * i + 3] = b.w;
+          const ulonglong2 a = __ldg(cr + i), b = __ldg(sr + i);
+          c[2 * i] = a.x, c[2 * i + 1] = a.y;
+          sn[2 * i] = b.x, sn[2 * i + 1] = b.y;
         }
       }
+    }
+    uint64_t w[4];
+    {
+      uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);  // ones
+      if (p.w[j] != nullptr && in_head) wv = __ldg(reinterpret_cast<const uint4*>(p.w[j] + 8 * sub));
+      unpack8(wv, w);
+    }
+    if (!PAIRS && p.cos != nullptr && !upper) {
+      // y[a] = n[a] cos - n[b] sin in the lower half of the pairs, n[b] cos + n[a] sin in the upper one
+#pragma unroll
+      for (int i = 0; i < kTable / 2; ++i) sn[i] ^= 0x8000000080000000ull;
     }
 
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int h = head0 + s * kPerStep;
-      float f[8], w[8];
+      uint64_t f[4];
       unpack8(v[s], f);
-      float sq = 0.0f;
+      uint64_t squares = mul2(f[0], f[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = fmaf(f[i], f[i], sq);
+      for (int i = 1; i < 4; ++i) squares = fma2(f[i], f[i], squares);
+      float sq, sq1;
+      unpair(squares, sq, sq1);
+      sq += sq1;
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xFFFFFFFFu, sq, o);
-      const float r = rsqrtf(fmaf(sq, p.inv_d, p.eps));
-      const int j = h >= p.heads[0];
-      unpack8(j ? wv[1] : wv[0], w);
+      const uint64_t r = both(rsqrtf(fmaf(sq, p.inv_d, p.eps)));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * r * w[i];
+      for (int i = 0; i < 4; ++i) f[i] = mul2(mul2(f[i], r), w[i]);
       if (p.cos != nullptr) {
         if constexpr (PAIRS) {
           if (turns) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float a = f[2 * i], b = f[2 * i + 1];
-              f[2 * i] = a * c[i] - b * sn[i];
-              f[2 * i + 1] = b * c[i] + a * sn[i];
+              float a, b, c0, c1, s0, s1;
+              unpair(f[i], a, b);
+              unpair(c[i / 2], c0, c1);
+              unpair(sn[i / 2], s0, s1);
+              const float ci = i & 1 ? c1 : c0, si = i & 1 ? s1 : s0;
+              f[i] = pair(a * ci - b * si, b * ci + a * si);
             }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float other = __shfl_sync(0xFFFFFFFFu, f[i], mate);
-            if (turns) f[i] = upper ? f[i] * c[i] + other * sn[i] : f[i] * c[i] - other * sn[i];
+          for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpair(f[i], a, b);
+            const uint64_t other = pair(__shfl_sync(0xFFFFFFFFu, a, mate), __shfl_sync(0xFFFFFFFFu, b, mate));
+            if (turns) f[i] = fma2(other, sn[i], mul2(f[i], c[i]));
           }
         }
       }
-      if (h < all_heads && in_head) {
-        const int hj = j ? h - p.heads[0] : h;
-        *reinterpret_cast<uint4*>(p.y[j] + m * p.ld_y[j] + hj * p.hs_y[j] + 8 * sub) = pack8(f);
-      }
+      if (h < heads && in_head) *reinterpret_cast<uint4*>(y + h * p.hs_y[j]) = pack8(f);
     }
   }
 }
@@ -259,7 +272,8 @@ extern "C" w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* d, w8a8_stream_t st
   int lanes = 2;
   while (8 * lanes < d->head_dim) lanes *= 2;
   const int per_unit = kSteps * (32 / lanes);
-  p.units = (heads[0] + heads[1] + per_unit - 1) / per_unit;
+  p.units_q = (heads[0] + per_unit - 1) / per_unit;
+  p.units = p.units_q + (heads[1] + per_unit - 1) / per_unit;
   const bool pairs = d->layout == W8A8_ROPE_PAIRS;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (lanes) {
