@@ -1,8 +1,8 @@
 // attention_sm100.cu -- attention for many queries, on the 5th-generation
 // tensor cores.
 //
-// A CTA takes 256 queries of one document and head, as two sub-tiles of 128
-// (the rows of a tcgen05.mma), and walks the keys a tile at a time:
+// A work item is 256 queries of one document and head, as two sub-tiles of
+// 128 (the rows of a tcgen05.mma); its keys are walked a tile at a time:
 //   S = Q K^T       Q and K from shared memory, S in tensor memory
 //   P = 2^(S c - m) rounded to bf16, in tensor memory
 //   O += P V        P from tensor memory, V from shared memory
@@ -22,6 +22,12 @@
 //   warp 19         zeroes the rows of the last V tile that lie behind the
 //                   document's end (a weight of 0 times whatever is there
 //                   must be 0)
+//
+// The grid has a CTA per item.  A CTA that runs takes over ones that have not
+// started (cluster launch control), so that an item's first loads and scores
+// run beside the epilogue of the one before, and the hardware's dynamic order
+// stays: items dealt out in a fixed way left some SMs an item more than
+// others (487 us against 422 at 2 x 4608 tokens, 24 heads of 128).
 //
 // S and P have columns of their own, so that S of the next tile is computed
 // while the softmax of this one runs, and the softmax warps never wait for a
@@ -58,13 +64,14 @@ constexpr float kGrowth = 8.0f;       // log2 of the growth of a row's maximum t
 // Blocks of 64 values (128 bytes) x rows: Q in sub-tiles of 128 rows, K and V in tiles of tile_keys rows.
 __host__ __device__ constexpr int q_bytes(int D) { return D / 64 * kSub * 128; }
 __host__ __device__ constexpr int tile_bytes(int D) { return D / 64 * tile_keys(D) * 128; }
-__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 7 : 8; }
+__host__ __device__ constexpr int ring_stages(int D) { return D == 128 ? 6 : 8; }
 // The softmax threads' exchange (two tiles' buffers of a float per half of the keys, sub-tile and query) and the
 // barriers, in front of Q and the ring, which are aligned to 1024 bytes.
 constexpr int kExchange = 2 * 2 * 2 * kSub;
 constexpr int kHeadBytes = 5 * 1024;
+constexpr int kStagingBytes = 2048;  // of a softmax warp's output
 __host__ __device__ constexpr int smem_bytes(int D) {
-  return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D);
+  return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D) + kSoftmaxWarps * kStagingBytes;
 }
 
 // tanh(y) = y * sum_n kTanh[n] y^2n on [-1, 1]: least squares on Chebyshev nodes, relative error 7e-7 in binary32.
@@ -113,40 +120,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kExchange * sizeof(float));
   uint64_t* empty = full + kStages;
   uint64_t* q_full = empty + kStages;   // [2]
-  uint64_t* s_full = q_full + 2;        // [2] scores ready
+  uint64_t* q_free = q_full + 2;        // [2] the item's last scores done
+  uint64_t* s_full = q_free + 2;        // [2] scores ready
   uint64_t* s_free = s_full + 2;        // [2] scores read
   uint64_t* p_full = s_free + 2;        // [2] weights ready
   uint64_t* o_full = p_full + 2;        // [2] product with V done: O complete so far, P free
+  // [2] a last V tile that ends inside has landed: two in turn, because the loader may be an item ahead of warp 19
+  // (not two: an item's Q waits for the last item's scores, and those for the product before them).
   uint64_t* tail_full = o_full + 2;
-  uint64_t* drain = tail_full + 1;      // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* drain = tail_full + 2;      // [2]
+  uint64_t* item_full = drain + 2;      // [2] the next item is known
+  uint64_t* item_free = item_full + 2;  // [2] ... and read by every warp
+  uint8_t* answer = smem + kHeadBytes - 32;  // [2][16]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(item_free + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* sQ = smem + kHeadBytes;
   uint8_t* ring = sQ + 2 * kQ;
+  uint8_t* staging = ring + kStages * kTile;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0);  // (known to be uniform)
   const int lane = threadIdx.x & 31;
 
-  // Causal documents: the slots with the most keys first, so that the last CTAs to start are short ones.
-  // Otherwise a head's slots side by side, which share its keys and values.
-  const int block = static_cast<int>(blockIdx.x);
-  const int head = p.causal ? block % p.heads_q : block / slots;
-  const int slot = p.causal ? slots - 1 - block / p.heads_q : block % slots;
-  const int d = slot_doc(p, slot, 1, kTileQ);
-  const Doc doc = load_doc(p, d);
-  const int row0 = (slot - slot_begin(p, d, 1, kTileQ)) * kTileQ;
-  const int rows = min(kTileQ, doc.lq - row0);
-  if (rows <= 0 || row0 < 0) return;  // an unused slot
-  const int kv_head = head / p.group;
-  // Key tiles of each sub-tile (limits grow with the query).
-  auto key_tiles = [&](int s) {
-    const int n = min(kSub, rows - s * kSub);
-    return n <= 0 ? 0 : (max(0, key_limit(p, doc, row0 + s * kSub + n - 1)) + kTileK - 1) / kTileK;
+  // A work item, the same for every warp (all lanes call it).  Causal documents: the slots with the most keys first, so
+  // that the last items are short ones.  Otherwise a head's slots side by side, which share its keys and values.
+  struct Item {
+    Doc doc;
+    int head, row0, rows;  // rows <= 0: an unused slot
+    int n0, n1, tiles;     // key tiles of each sub-tile (limits grow with the query) and of the item
+    int tail_rows;         // rows of the last V tile that are the document's
+    bool tail;             // ... and not all of them
   };
-  const int n0 = key_tiles(0), n1 = key_tiles(1);
-  const int tiles = max(n0, n1);
-  const int tail_rows = doc.lk - (tiles - 1) * kTileK;  // rows of the last V tile that are the document's
-  const bool tail = tiles > 0 && tail_rows < kTileK;
+  const auto item_of = [&](int x) {
+    Item it;
+    it.head = p.causal ? x % p.heads_q : x / slots;
+    const int slot = p.causal ? slots - 1 - x / p.heads_q : x % slots;
+    const int d = slot_doc(p, slot, 1, kTileQ);
+    it.doc = load_doc(p, d);
+    it.row0 = (slot - slot_begin(p, d, 1, kTileQ)) * kTileQ;
+    it.rows = it.row0 < 0 ? 0 : min(kTileQ, it.doc.lq - it.row0);
+    const auto key_tiles = [&](int s) {
+      const int n = min(kSub, it.rows - s * kSub);
+      return n <= 0 ? 0 : (max(0, key_limit(p, it.doc, it.row0 + s * kSub + n - 1)) + kTileK - 1) / kTileK;
+    };
+    it.n0 = key_tiles(0);
+    it.n1 = key_tiles(1);
+    it.tiles = max(it.n0, it.n1);
+    it.tail_rows = it.doc.lk - (it.tiles - 1) * kTileK;
+    it.tail = it.tiles > 0 && it.tail_rows < kTileK;
+    return it;
+  };
+  // The items of this CTA, one after the other, in every warp: the first is the CTA's own, the next ones come into two
+  // buffers in turn.
+  int item = static_cast<int>(blockIdx.x), taken = 0;
+  const auto next_item = [&](bool ok) {  // all lanes; -1 behind the last one, or if !ok
+    if (!ok) return -1;
+    ++taken;
+    const int b = taken & 1;
+    const bool got = mbar_wait_bounded(&item_full[b], static_cast<uint32_t>((taken - 1) >> 1) & 1u, abort_flag,
+                                       p.timeout_ns, err, kSiteAttnItem);
+    if (!__all_sync(0xFFFFFFFFu, got)) return -1;
+    const int x = launch_cancelled(answer + 16 * b);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_free[b]);
+    return x;
+  };
 
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled tiles need it; a kernel without static shared memory has it
     if (threadIdx.x == 0) record_timeout(err, kSiteAttnLoad);
@@ -158,14 +195,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], 2);  // both issuers
     }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&tail_full[s], 1);
       mbar_init(&drain[s], 1);
+      mbar_init(&item_full[s], 1);
+      mbar_init(&item_free[s], kThreads / 32);
       mbar_init(&q_full[s], 1);
+      mbar_init(&q_free[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_free[s], kSoftmaxWarps / 2);
       mbar_init(&p_full[s], kSoftmaxWarps / 2);
       mbar_init(&o_full[s], 1);
     }
-    mbar_init(tail_full, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -185,137 +225,164 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kSoftmaxWarps) {
     reg_lower<kRegsOther>();
-    // One thread each: a warp that votes, elects and converges around every wait spends most of a tile's time on
-    // that.
+    // One thread each loads and issues: a warp that votes, elects and converges around every wait spends most of a
+    // tile's time on that.
     const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       return mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
     };
-    if (warp == 16 && elect_one()) {
+    bool ok = true;
+    if (warp == 16) {
       // ------------------------------------------------------------ loader
       const uint64_t keep = l2_policy_evict_last();
       const uint64_t once = l2_policy_evict_first();
-      // Fills in the order of their use: K of tile 0, then K of tile j + 1 and V of tile j.
-      int stage = 0, fills = 0;
-      uint32_t phase = 1;
-      bool ok = true;
-      const auto load_q = [&](int s) {
-        mbar_arrive_expect_tx(&q_full[s], kQ);
-        for (int b = 0; b < kBlocks; ++b) {
-          tma_load_3d_hint(sQ + s * kQ + b * kQBlock, &tm_q, &q_full[s], 64 * b, doc.q0 + row0 + s * kSub, head, once);
-        }
-      };
-      const auto load = [&](const CUtensorMap* map, int tile, uint64_t* landed) {
-        ok = wait(&empty[stage], phase, kSiteAttnLoad);
-        if (!ok) return;
-        if (landed == nullptr) landed = &full[stage];
-        mbar_arrive_expect_tx(landed, kTile);
+      int stage = 0;
+      uint32_t phase = 1, q_phase[2] = {1, 1};
+      int tails = 0;
+      for (; item >= 0; item = next_item(ok)) {
+        const Item it = item_of(item);
+        if (elect_one()) {
+          const int kv_head = it.head / p.group;
+          const auto load_q = [&](int s) {
+            ok = ok && wait(&q_free[s], q_phase[s], kSiteAttnLoad);
+            if (!ok) return;
+            q_phase[s] ^= 1u;
+            mbar_arrive_expect_tx(&q_full[s], kQ);
+            for (int b = 0; b < kBlocks; ++b) {
+              tma_load_3d_hint(sQ + s * kQ + b * kQBlock, &tm_q, &q_full[s], 64 * b, it.doc.q0 + it.row0 + s * kSub,
+                               it.head, once);
+            }
+          };
+          const auto load = [&](const CUtensorMap* map, int tile, uint64_t* landed) {
+            ok = ok && wait(&empty[stage], phase, kSiteAttnLoad);
+            if (!ok) return;
+            if (landed == nullptr) landed = &full[stage];
+            mbar_arrive_expect_tx(landed, kTile);
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          tma_load_3d_hint(ring + stage * kTile + b * kBlock, map, landed, 64 * b, doc.k0 + tile * kTileK, kv_head,
-                           keep);
+            for (int b = 0; b < kBlocks; ++b) {
+              tma_load_3d_hint(ring + stage * kTile + b * kBlock, map, landed, 64 * b, it.doc.k0 + tile * kTileK,
+                               kv_head, keep);
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          };
+          // Fills in the order of their use: K of tile 0, then K of tile j + 1 and V of tile j.
+          if (it.tiles > 0) load(&tm_k, 0, nullptr);
+          if (it.n0 > 0) load_q(0);
+          if (it.n1 > 0) load_q(1);
+          for (int j = 0; ok && j < it.tiles; ++j) {
+            if (j + 1 < it.tiles) load(&tm_k, j + 1, nullptr);
+            // (a last V tile that ends inside goes to warp 19 first, which fills the slot)
+            load(&tm_v, j, it.tail && j + 1 == it.tiles ? &tail_full[tails & 1] : nullptr);
+          }
+          tails += it.tail;
+          // The item after this one, asked for with the last loads of this one (earlier, and items are dealt out before
+          // it is known who is done first).  Its buffer has been read by every warp.
+          const int asked = taken + 1, b = asked & 1;
+          ok = ok && (asked <= 2 || wait(&item_free[b], static_cast<uint32_t>((asked - 3) >> 1) & 1u, kSiteAttnItem));
+          if (ok) {
+            fence_proxy_async_smem();
+            mbar_arrive_expect_tx(&item_full[b], 16);
+            launch_cancel_async(answer + 16 * b, &item_full[b]);
+          }
         }
-        ++fills;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      if (n0 > 0) load_q(0);
-      if (tiles > 0) load(&tm_k, 0, nullptr);
-      if (n1 > 0) load_q(1);
-      for (int j = 0; ok && j < tiles; ++j) {
-        if (j + 1 < tiles) load(&tm_k, j + 1, nullptr);
-        // (a last V tile that ends inside goes to warp 19 first, which fills the slot)
-        if (ok) load(&tm_v, j, tail && j + 1 == tiles ? tail_full : nullptr);
+        ok = __all_sync(0xFFFFFFFFu, ok);
       }
-      // Every load must have landed before the CTA ends (on the normal path they have).
-      for (int f = max(0, fills - kStages); f < fills; ++f) {
-        if (tail && f == 2 * tiles - 1) {
-          mbar_wait_drain(tail_full, 0, p.timeout_ns, err);
-        } else {
-          mbar_wait_drain(&full[f % kStages], static_cast<uint32_t>((f / kStages) & 1), p.timeout_ns, err);
-        }
-      }
-      if (n0 > 0) mbar_wait_drain(&q_full[0], 0, p.timeout_ns, err);
-      if (n1 > 0) mbar_wait_drain(&q_full[1], 0, p.timeout_ns, err);
-    } else if ((warp == 17 || warp == 18) && elect_one()) {
+    } else if (warp == 17 || warp == 18) {
       // -------------------------------------------------------- MMA issuer
       const int s = warp - 17;
-      const int n = s == 0 ? n0 : n1;
-      bool ok = true;
       // Matrix descriptors: the high words are constant, the low ones hold the address (in units of 16 bytes).
       const uint64_t desc_q = make_smem_desc_k_sw128(smem_u32(sQ + s * kQ));
       const uint64_t desc_k = make_smem_desc_k_sw128(smem_u32(ring)), desc_v = make_smem_desc_n_sw128(smem_u32(ring), kBlock);
       const uint32_t t_s = tmem + s * kSpan, t_o = tmem + kColO + s * D;
       int stage = 0;
-      uint32_t phase = 0;
-      const auto wait_fill = [&] { ok = wait(&full[stage], phase, kSiteAttnOperand); };
-      const auto release = [&] {  // the ring slot is free when the MMAs issued so far are done
-        mma_commit(&empty[stage]);
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      const auto scores = [&] {  // S = Q K^T
-        const uint64_t kd = desc_k + stage * (kTile / 16);
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          mma_bf16_ss(t_s, desc_q + ((x / 4) * (kQBlock / 16) + 2 * (x % 4)),
-                      kd + ((x / 4) * (kBlock / 16) + 2 * (x % 4)), kIdescS, x > 0);
-        }
-        mma_commit(&s_full[s]);
-      };
-      if (tiles > 0) {
-        wait_fill();
-        if (ok && n > 0) {
-          ok = wait(&q_full[s], 0, kSiteAttnOperand);
-          if (ok) scores();
-        }
-        if (ok) release();
-      }
-      for (int j = 0; ok && j < tiles; ++j) {
-        const uint32_t parity = static_cast<uint32_t>(j & 1);
-        if (j + 1 < tiles) {
-          wait_fill();
-          if (ok && j + 1 < n) {
-            ok = wait(&s_free[s], parity, kSiteAttnWeights);
+      uint32_t phase = 0, q_phase = 0;
+      uint32_t s_phase = 1, p_phase = 0;  // of s_free (one phase behind s_full) and p_full
+      for (; item >= 0; item = next_item(ok)) {
+        const Item it = item_of(item);
+        if (elect_one()) {
+          const int n = s == 0 ? it.n0 : it.n1;
+          const auto wait_fill = [&] { ok = ok && wait(&full[stage], phase, kSiteAttnOperand); };
+          const auto release = [&] {  // the ring slot is free when the MMAs issued so far are done
+            mma_commit(&empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          };
+          const auto scores = [&](int j) {  // S = Q K^T
+            ok = ok && wait(&s_free[s], s_phase, kSiteAttnWeights);
+            if (!ok) return;
+            s_phase ^= 1u;
             tc_fence_after_sync();
-            if (ok) scores();
-          }
-          if (!ok) break;
-          release();
-        }
-        wait_fill();
-        if (ok && j < n) {
-          ok = wait(&p_full[s], parity, kSiteAttnWeights);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t vd = desc_v + stage * (kTile / 16);
+            const uint64_t kd = desc_k + stage * (kTile / 16);
 #pragma unroll
-          for (int x = 0; x < kTileK / 16; ++x) {
-            mma_bf16_ts(t_o, t_s + kTileK + 8 * x, vd + 128 * x, kIdescO, (x > 0 || j > 0) ? 1u : 0u);
+            for (int x = 0; x < D / 16; ++x) {
+              mma_bf16_ss(t_s, desc_q + ((x / 4) * (kQBlock / 16) + 2 * (x % 4)),
+                          kd + ((x / 4) * (kBlock / 16) + 2 * (x % 4)), kIdescS, x > 0);
+            }
+            mma_commit(&s_full[s]);
+            if (j + 1 == n) mma_commit(&q_free[s]);
+          };
+          // Step j: the scores of tile j, then the product of tile j - 1.
+#pragma unroll 1
+          for (int j = 0; ok && j <= it.tiles && it.tiles > 0; ++j) {
+            if (j < it.tiles) {
+              wait_fill();
+              if (ok && j == 0 && n > 0) {
+                ok = wait(&q_full[s], q_phase, kSiteAttnOperand);
+                q_phase ^= 1u;
+              }
+              if (j < n) scores(j);
+              if (!ok) break;
+              release();
+            }
+            if (j == 0) continue;
+            wait_fill();
+            if (j - 1 < n) {
+              ok = ok && wait(&p_full[s], p_phase, kSiteAttnWeights);
+              if (!ok) break;
+              p_phase ^= 1u;
+              tc_fence_after_sync();
+              const uint64_t vd = desc_v + stage * (kTile / 16);
+#pragma unroll
+              for (int x = 0; x < kTileK / 16; ++x) {
+                mma_bf16_ts(t_o, t_s + kTileK + 8 * x, vd + 128 * x, kIdescO, (x > 0 || j > 1) ? 1u : 0u);
+              }
+              mma_commit(&o_full[s]);
+            }
+            if (ok) release();
           }
-          mma_commit(&o_full[s]);
         }
-        if (ok) release();
+        ok = __all_sync(0xFFFFFFFFu, ok);
       }
       // No MMA may still run when tensor memory is freed.
-      mma_commit(&drain[s]);
-      mbar_wait_drain(&drain[s], 0, p.timeout_ns, err);
-    } else if (warp == 19 && tail) {
-      // ------------------------------------------------ end of the document
-      const int stage = (2 * tiles - 1) % kStages;
-      if (warp_wait(tail_full, 0, abort_flag, p.timeout_ns, err, kSiteAttnOperand)) {
+      if (elect_one()) {
+        mma_commit(&drain[s]);
+        mbar_wait_drain(&drain[s], 0, p.timeout_ns, err);
+      }
+    } else {
+      // ------------------------------------------------ ends of documents
+      int fills = 0, tails = 0;
+      for (; item >= 0; item = next_item(ok)) {
+        const Item it = item_of(item);
+        fills = (fills + 2 * it.tiles) % kStages;  // the ring slot behind the item's last V tile
+        if (!it.tail) continue;
+        ok = warp_wait(&tail_full[tails & 1], static_cast<uint32_t>(tails >> 1) & 1u, abort_flag, p.timeout_ns, err,
+                       kSiteAttnOperand);
+        if (!ok) continue;
+        ++tails;
+        const int stage = (fills + kStages - 1) % kStages;
         uint8_t* v = ring + stage * kTile;
-        for (int x = tail_rows * 8 + lane; x < kTileK * 8; x += 32) {
+        for (int e = it.tail_rows * 8 + lane; e < kTileK * 8; e += 32) {
 #pragma unroll
-          for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4*>(v + b * kBlock + x * 16) = make_uint4(0, 0, 0, 0);
+          for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4*>(v + b * kBlock + e * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[stage]);
     }
     __syncwarp();
   } else {
@@ -325,229 +392,243 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int part = (warp >> 2) & 1;  // keys kHalf * part .. of every tile
     const int quarter = warp & 3;
     const uint32_t partners = 1 + (warp >> 3) * 4 + quarter;  // named barrier of the two warps of 32 queries
-    const int my_rows = min(kSub, rows - s * kSub);  // <= 0: nothing in this sub-tile
-    const int n = s == 0 ? n0 : n1;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lanes + s * kSpan + kHalf * part;
     const uint32_t t_p = tmem + lanes + s * kSpan + kTileK + kHalf / 2 * part;
     const uint32_t t_o = tmem + lanes + kColO + s * D + D / 2 * part;
     const int in_sub = quarter * 32 + lane;
-    const int i = row0 + s * kSub + in_sub;  // the thread's query
-    const int limit = in_sub < my_rows ? max(0, key_limit(p, doc, i)) : 0;
-    const int least = my_rows > 0 ? key_limit(p, doc, row0 + s * kSub) : 0;  // the sub-tile's smallest limit
     constexpr bool kChange = CAP || BIAS;  // scores need more than the factor c
     const float c = p.scale * kLog2e;
     const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
     const float c_tanh = 2.0f * kLog2e * inv_cap;
     const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
-    const float slope = BIAS ? __ldg(p.slopes + head) * kLog2e : 0.0f;
-    const int place = i + doc.shift;
-    const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
-
-    // Scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
-    const auto first_pass = [&](auto& v, int key0, bool masked) {
-      constexpr int N = sizeof(v) / sizeof(v[0]);
-      if constexpr (CAP) {
-        // Scores within the cap on either side (all of them, unless the scores are far beyond it) take the
-        // polynomial for tanh; others two special functions each.
-        float far = 0.0f;
-#pragma unroll
-        for (int x = 0; x < N; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
-        if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
-#pragma unroll
-          for (int x = 0; x < N; x += 2) {
-            const uint64_t y = mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), both(inv_cap));
-            const uint64_t u = mul2(y, y);
-            uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
-            t = fma2(t, u, both(kTanh[3]));
-            t = fma2(t, u, both(kTanh[2]));
-            t = fma2(t, u, both(kTanh[1]));
-            t = fma2(t, u, both(kTanh[0]));
-            float a0, a1;
-            unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
-            v[x] = __float_as_uint(a0);
-            v[x + 1] = __float_as_uint(a1);
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
-        }
-      }
-      if constexpr (BIAS) {
-        const float f = CAP ? 1.0f : c;
-        const float first = static_cast<float>(key0 - place);  // distance of the first key, signed
-        if (key0 + N - 1 <= first_place) {
-          // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
-          const float at0 = slope * first;
-#pragma unroll
-          for (int x = 0; x < N; ++x) {
-            v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, fmaf(slope, static_cast<float>(x), at0)));
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < N; ++x) {
-            v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, -slope * fabsf(first + static_cast<float>(x))));
-          }
-        }
-      }
-      if (masked) {
-        const int left = limit - key0;
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-          if (x >= left) v[x] = 0xFF800000u;  // -inf
-        }
-      }
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int x = 0; x < N; x += 4) {
-        top[0] = max3(top[0], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-        top[1] = max3(top[1], __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
-      }
-      return fmax_nan(top[0], top[1]);
-    };
-
-    // The value of the thread with the other half of this query's keys.  One barrier is enough with two buffers in
-    // turn: a buffer is written again behind the next tile's barrier, where the partner has read it.  (A warp that
-    // aborts arrives once more, and its partner looks at the flag before it comes back, so that none is left waiting.)
-    const auto partner = [&](float x, int turn) {
-      float* const at = exchange + (turn & 1) * (4 * kSub) + s * kSub + in_sub;
-      at[part * 2 * kSub] = x;
-      named_barrier_sync(partners, 64);
-      return at[(part ^ 1) * 2 * kSub];
-    };
-    const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-      const bool done = mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
-      return __all_sync(0xFFFFFFFFu, done && !*abort_flag);
-    };
-
-    float m = -INFINITY;  // in units of log2
-    float l = 0.0f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = wait(&s_full[s], static_cast<uint32_t>(j & 1), kSiteAttnScores);
+    uint32_t s_phase = 0, o_phase = 0;  // of s_full and o_full
+    int turn = 0;                       // of the exchange buffers
+
+    for (; item >= 0; item = next_item(ok)) {
+      const Item it = item_of(item);
+      const Doc& doc = it.doc;
+      const int head = it.head, row0 = it.row0;
+      const int my_rows = min(kSub, it.rows - s * kSub);  // <= 0: nothing in this sub-tile
+      if (my_rows <= 0) continue;
+      const int n = s == 0 ? it.n0 : it.n1;
+      const int i = row0 + s * kSub + in_sub;  // the thread's query
+      const int limit = in_sub < my_rows ? max(0, key_limit(p, doc, i)) : 0;
+      const int least = key_limit(p, doc, row0 + s * kSub);  // the sub-tile's smallest limit
+      const float slope = BIAS ? __ldg(p.slopes + head) * kLog2e : 0.0f;
+      const int place = i + doc.shift;
+      const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
+
+      // Scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
+      const auto first_pass = [&](auto& v, int key0, bool masked) {
+        constexpr int N = sizeof(v) / sizeof(v[0]);
+        if constexpr (CAP) {
+          // Scores within the cap on either side (all of them, unless the scores are far beyond it) take the
+          // polynomial for tanh; others two special functions each.
+          float far = 0.0f;
+#pragma unroll
+          for (int x = 0; x < N; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
+          if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
+#pragma unroll
+            for (int x = 0; x < N; x += 2) {
+              const uint64_t y = mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), both(inv_cap));
+              const uint64_t u = mul2(y, y);
+              uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
+              t = fma2(t, u, both(kTanh[3]));
+              t = fma2(t, u, both(kTanh[2]));
+              t = fma2(t, u, both(kTanh[1]));
+              t = fma2(t, u, both(kTanh[0]));
+              float a0, a1;
+              unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
+              v[x] = __float_as_uint(a0);
+              v[x + 1] = __float_as_uint(a1);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
+          }
+        }
+        if constexpr (BIAS) {
+          const float f = CAP ? 1.0f : c;
+          const float first = static_cast<float>(key0 - place);  // distance of the first key, signed
+          if (key0 + N - 1 <= first_place) {
+            // No key lies ahead of any query of the sub-tile: the bias is linear in the key.
+            const float at0 = slope * first;
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+              v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, fmaf(slope, static_cast<float>(x), at0)));
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+              v[x] = __float_as_uint(fmaf(__uint_as_float(v[x]), f, -slope * fabsf(first + static_cast<float>(x))));
+            }
+          }
+        }
+        if (masked) {
+          const int left = limit - key0;
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            if (x >= left) v[x] = 0xFF800000u;  // -inf
+          }
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < N; x += 4) {
+          top[0] = max3(top[0], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+          top[1] = max3(top[1], __uint_as_float(v[x + 2]), __uint_as_float(v[x + 3]));
+        }
+        return fmax_nan(top[0], top[1]);
+      };
+
+      // The value of the thread with the other half of this query's keys.  One barrier is enough with two buffers in
+      // turn: a buffer is written again behind the next tile's barrier, where the partner has read it.  (A warp that
+      // aborts arrives once more, and its partner looks at the flag before it comes back, so that none is left waiting.)
+      const auto partner = [&](float x) {
+        float* const at = exchange + (turn & 1) * (4 * kSub) + s * kSub + in_sub;
+        ++turn;
+        at[part * 2 * kSub] = x;
+        named_barrier_sync(partners, 64);
+        return at[(part ^ 1) * 2 * kSub];
+      };
+      const auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+        const bool done = mbar_wait_bounded(bar, parity, abort_flag, p.timeout_ns, err, site);
+        return __all_sync(0xFFFFFFFFu, done && !*abort_flag);
+      };
+
+      float m = -INFINITY;  // in units of log2
+      float l = 0.0f;
+      for (int j = 0; j < n; ++j) {
+        ok = wait(&s_full[s], s_phase, kSiteAttnScores);
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after_sync();
+        const bool masked = (j + 1) * kTileK > least;
+        const int key0 = j * kTileK + kHalf * part;
+        uint32_t va[32], vb[kHalf - 32];
+        tmem_load_cols_async(t_s, va);
+        tmem_load_cols_async(t_s + 32, vb);
+        tmem_wait_loads(va);
+        tmem_wait_loads(vb);
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[s]);
+        float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
+        top = fmax_nan(top, partner(top));
+        if (!kChange) top *= c;  // c > 0
+        // P and O are free when the last tile's product is done.  (To wait here, rather than behind the exponentials,
+        // keeps the two sub-tiles out of step: 427 us against 448 for 2 x 4608 tokens, 24 heads of 128.  When both
+        // compute exponentials at the same time, both come to wait at the same time.)
+        if (j > 0) {
+          ok = wait(&o_full[s], o_phase, kSiteAttnOut);
+          if (!ok) break;
+          o_phase ^= 1u;
+          tc_fence_after_sync();
+        }
+        if (j == 0) {
+          m = top;
+        } else {
+          const bool grow = !(top <= m + kGrowth);  // (a NaN reaches O and l, and stays there)
+          if (__any_sync(0xFFFFFFFFu, grow)) {      // (the same in both warps)
+            const float f = grow ? ex2(m - top) : 1.0f;
+            if (grow) m = top;
+            l *= f;
+#pragma unroll 1
+            for (int b = 0; b < D / 32; ++b) {
+              uint32_t o[16];
+              tmem_load_16cols(t_o + 16 * b, o);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_store_cols(t_o + 16 * b, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.0f : m;
+        const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
+        uint64_t sums[2] = {both(0.0f), both(0.0f)};
+        // Weights of 2 N keys.  (A part of the exponentials as polynomials on the FMA units, to relieve the special-function
+        // units, made it slower: 438 us against 427 with an eighth of them, 453 with three eighths, at 2 x 4608 tokens, 24
+        // heads of 128.  Two warps per scheduler do not hide the polynomial's latency.)
+        const auto weights = [&](const uint32_t* v, auto& w) {
+          constexpr int N = sizeof(w) / sizeof(w[0]);
+#pragma unroll
+          for (int x = 0; x < N; ++x) {
+            const uint64_t y = pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
+            const uint64_t e = kChange ? add2(y, minus) : fma2(y, c2, minus);
+            float a0, a1;
+            unpair(e, a0, a1);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            sums[x & 1] = add2(sums[x & 1], pair(a0, a1));
+            w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
+          }
+        };
+        uint32_t wa[16], wb[kHalf / 2 - 16];
+        weights(va, wa);
+        weights(vb, wb);
+        tmem_store_cols(t_p, wa);
+        tmem_store_cols(t_p + 16, wb);
+        tmem_wait_store();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[s]);
+        float s0, s1;
+        unpair(add2(sums[0], sums[1]), s0, s1);
+        l += s0 + s1;
+      }
+
+      // ------------------------------------------------------------- epilogue
+      if (ok && n > 0) {
+        ok = wait(&o_full[s], o_phase, kSiteAttnOut);
+        o_phase ^= 1u;
+      }
       if (!ok) break;
       tc_fence_after_sync();
-      const bool masked = (j + 1) * kTileK > least;
-      const int key0 = j * kTileK + kHalf * part;
-      uint32_t va[32], vb[kHalf - 32];
-      tmem_load_cols_async(t_s, va);
-      tmem_load_cols_async(t_s + 32, vb);
-      tmem_wait_loads(va);
-      tmem_wait_loads(vb);
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[s]);
-      float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
-      top = fmax_nan(top, partner(top, j));
-      if (!kChange) top *= c;  // c > 0
-      // P and O are free when the last tile's product is done.  (To wait here, rather than behind the exponentials,
-      // keeps the two sub-tiles out of step: 427 us against 448 for 2 x 4608 tokens, 24 heads of 128.  When both
-      // compute exponentials at the same time, both come to wait at the same time.)
-      if (j > 0) {
-        ok = wait(&o_full[s], static_cast<uint32_t>(j - 1) & 1u, kSiteAttnOut);
-        if (!ok) break;
-        tc_fence_after_sync();
-      }
-      if (j == 0) {
-        m = top;
-      } else {
-        const bool grow = !(top <= m + kGrowth);  // (a NaN reaches O and l, and stays there)
-        if (__any_sync(0xFFFFFFFFu, grow)) {      // (the same in both warps)
-          const float f = grow ? ex2(m - top) : 1.0f;
-          if (grow) m = top;
-          l *= f;
-#pragma unroll 1
-          for (int b = 0; b < D / 32; ++b) {
-            uint32_t o[16];
-            tmem_load_16cols(t_o + 16 * b, o);
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-            tmem_store_cols(t_o + 16 * b, o);
-          }
-        }
-      }
-      const float base = m == -INFINITY ? 0.0f : m;
-      const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
-      uint64_t sums[2] = {both(0.0f), both(0.0f)};
-      // Weights of 2 N keys.  (A part of the exponentials as polynomials on the FMA units, to relieve the special-function
-      // units, made it slower: 438 us against 427 with an eighth of them, 453 with three eighths, at 2 x 4608 tokens, 24
-      // heads of 128.  Two warps per scheduler do not hide the polynomial's latency.)
-      const auto weights = [&](const uint32_t* v, auto& w) {
-        constexpr int N = sizeof(w) / sizeof(w[0]);
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-          const uint64_t y = pair(__uint_as_float(v[2 * x]), __uint_as_float(v[2 * x + 1]));
-          const uint64_t e = kChange ? add2(y, minus) : fma2(y, c2, minus);
-          float a0, a1;
-          unpair(e, a0, a1);
-          a0 = ex2(a0);
-          a1 = ex2(a1);
-          sums[x & 1] = add2(sums[x & 1], pair(a0, a1));
-          w[x] = pack_bf16(a0, a1);  // the weights' one rounding; their sum is that of the unrounded ones
-        }
-      };
-      uint32_t wa[16], wb[kHalf / 2 - 16];
-      weights(va, wa);
-      weights(vb, wb);
-      tmem_store_cols(t_p, wa);
-      tmem_store_cols(t_p + 16, wb);
-      tmem_wait_store();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
-      float s0, s1;
-      unpair(add2(sums[0], sums[1]), s0, s1);
-      l += s0 + s1;
-    }
-
-    // ------------------------------------------------------------- epilogue
-    if (ok && n > 0) ok = wait(&o_full[s], static_cast<uint32_t>(n - 1) & 1u, kSiteAttnOut);
-    if (!ok) named_barrier_arrive(partners, 64);  // the partner may stand at its barrier: it will see the abort next
-    if (ok && my_rows > 0) {
-      tc_fence_after_sync();
-      l += partner(l, n);
+      if (n > 0) l += partner(l);
       const bool any = limit > 0;
       const float inv = any ? 1.0f / l : 0.0f;
-      // The warp's 32 rows x D/2 values through shared memory (its part of the sub-tile's Q, which no MMA reads any
-      // more), so that they leave in whole segments of D bytes.
-      constexpr int kVec = D / 16;  // 16-byte vectors of a row
-      uint8_t* stage = sQ + s * kQ + (part * 4 + quarter) * 32 * D;
+      const int64_t token = doc.q0 + i;
+      // The warp's 32 rows x D/2 values, 32 columns at a time through shared memory, so that they leave in segments of 64
+      // bytes (16 bytes a thread, each in a row of its own, keep the load/store units busy for 4 000 cycles an item).
+      uint8_t* stage = staging + warp * kStagingBytes;
+      const int64_t token0 = doc.q0 + row0 + s * kSub + quarter * 32;
+      const int valid = my_rows - quarter * 32;
 #pragma unroll 1
-      for (int b = 0; b < D / 32; ++b) {
-        uint32_t o[16];
+      for (int b = 0; b < D / 64; ++b) {
+        uint32_t o[32];
         if (n > 0) {
-          tmem_load_16cols(t_o + 16 * b, o);
+          tmem_load_32cols(t_o + 32 * b, o);
         } else {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] = 0u;
+          for (int y = 0; y < 32; ++y) o[y] = 0u;
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int y = 0; y < 4; ++y) {
           uint32_t w[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float a0 = __uint_as_float(o[8 * x + 2 * y]) * inv, a1 = __uint_as_float(o[8 * x + 2 * y + 1]) * inv;
-            w[y] = any ? pack_bf16(a0, a1) : 0u;
+          for (int z = 0; z < 4; ++z) {
+            const float a0 = __uint_as_float(o[8 * y + 2 * z]) * inv, a1 = __uint_as_float(o[8 * y + 2 * z + 1]) * inv;
+            w[z] = any ? pack_bf16(a0, a1) : 0u;
           }
-          *reinterpret_cast<uint4*>(stage + lane * D + (((2 * b + x) ^ (lane & (kVec - 1))) * 16)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + (4 * lane + (y ^ ((lane >> 1) & 3))) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-      }
-      __syncwarp();
-      const int64_t token0 = doc.q0 + row0 + s * kSub + quarter * 32;
-      const int valid = min(32, my_rows - quarter * 32);
-#pragma unroll 4
-      for (int e = lane; e < 32 * kVec; e += 32) {
-        const int r = e / kVec, x = e % kVec;
-        if (r < valid) {
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * D + ((x ^ (r & (kVec - 1))) * 16));
-          *reinterpret_cast<uint4*>(p.out + (token0 + r) * p.ldo + head * p.hso + D / 2 * part + x * 8) = w;
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int r = 8 * y + (lane >> 2), z = lane & 3;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + (4 * r + (z ^ ((r >> 1) & 3))) * 16);
+          if (r < valid) {
+            *reinterpret_cast<uint4*>(p.out + (token0 + r) * p.ldo + head * p.hso + D / 2 * part + 32 * b + 8 * z) = w;
+          }
         }
+        __syncwarp();
       }
       if (p.lse != nullptr && part == 0 && in_sub < my_rows) {
-        p.lse[(token0 + lane) * p.heads_q + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[token * p.heads_q + head] = any ? (m + log2f(l)) * kLn2 : -INFINITY;
       }
     }
+    if (!ok) named_barrier_arrive(partners, 64);  // the partner may stand at its barrier: it will see the abort next
   }
 
   tc_fence_before_sync();
@@ -585,14 +666,14 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
-  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 13) * 8 + 8 <= kHeadBytes, "shared memory");
+  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 20) * 8 + 8 <= kHeadBytes - 32, "shared memory");
   static std::atomic<uint64_t> set{0};
   e = allow_shared_memory(kernel, smem, set);
   if (e != cudaSuccess) return e;
   const int64_t slots = p.tokens_q / kTileQ + p.docs;
-  if (slots * p.heads_q > 2147483647) return cudaErrorInvalidValue;
-  kernel<<<static_cast<unsigned>(slots * p.heads_q), kThreads, smem, stream>>>(tm_q, tm_k, tm_v, p,
-                                                                              static_cast<int>(slots), err);
+  const int64_t items = slots * p.heads_q;
+  if (items > 2147483647) return cudaErrorInvalidValue;
+  kernel<<<static_cast<unsigned>(items), kThreads, smem, stream>>>(tm_q, tm_k, tm_v, p, static_cast<int>(slots), err);
   return cudaGetLastError();
 }
 

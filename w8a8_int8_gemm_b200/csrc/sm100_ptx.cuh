@@ -26,6 +26,7 @@ enum WaitSite : int {
   kSiteAttnWeights = 10,    // attention: MMA issuer waiting for a tile of weights
   kSiteAttnScores = 11,     // attention: softmax waiting for a tile of scores
   kSiteAttnOut = 12,        // attention: softmax waiting for the weighted sum
+  kSiteAttnItem = 13,       // attention: waiting for the next work item
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -527,6 +528,33 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, uint64_t
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+
+// ------------------------------------------- work stealing by launch control
+
+// Ask for a CTA of this grid that has not started yet, to be done by this CTA
+// in its place: 16 bytes at `response` (16-byte aligned), counted on `bar`.
+__device__ __forceinline__ void launch_cancel_async(void* response, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(response)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+
+// The answer: its blockIdx.x, or -1 (every CTA has started).
+__device__ __forceinline__ int launch_cancelled(const void* response) {
+  uint32_t got, x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  return got != 0 ? static_cast<int>(x) : -1;
 }
 
 // Registers per thread of this warpgroup (a multiple of 8; all its warps execute it).
