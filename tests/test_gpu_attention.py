@@ -139,6 +139,20 @@ def test_sharp_and_flat_weights(w8, scale, std):
     case(w8, [(140, 400), (3, 300)], 2, 1, 128, scale=scale, std=std, causal=True)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [1e-3, 0.3, 4.0, 50.0, 700.0, 1e5])
+def test_cap_over_its_range(w8, cap, D):
+    """Scores far inside the cap, around it and far beyond it, in the same tile and in tiles of their own."""
+    for Lq in (2, 150):
+        q, k, v = tensor(Lq, 2, D), tensor(450, 2, D, seed=2), tensor(450, 2, D, seed=3)
+        q[: Lq // 2] *= 0.02
+        k[:130] *= 0.05
+        k[300:] *= 4.0
+        lse = torch.empty(Lq, 2, device=DEV)
+        out = w8.w8a8_attention(q, k, v, cap=cap, lse=lse)
+        check(out, lse, q, k, v, [0, Lq], [0, 450], D ** -0.5, cap=cap)
+
+
 def test_scores_that_climb(w8):
     """The running maximum grows with every tile of keys, by more and less than a power of 2^8 at a time."""
     for step in (0.02, 0.5):

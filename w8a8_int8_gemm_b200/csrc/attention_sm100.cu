@@ -44,6 +44,7 @@
 #include <cuda.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "internal.h"
@@ -74,9 +75,11 @@ __host__ __device__ constexpr int smem_bytes(int D) {
   return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D) + kSoftmaxWarps * kStagingBytes;
 }
 
-// tanh(y) = y * sum_n kTanh[n] y^2n on [-1, 1]: least squares on Chebyshev nodes, relative error 7e-7 in binary32.
+// tanh(y) = y * sum_n k[n] y^2n, least squares on Chebyshev nodes: relative error 7e-7 (evaluated in binary32) for
+// |y| <= 1 with kTanh and |y| <= 1/4 with kTanhNear.
 __device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
                                        -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
+__device__ constexpr float kTanhNear[3] = {9.9999960187e-1f, -3.3321876803e-1f, 1.2841111966e-1f};
 
 // Maximum of three; NaN if one is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -402,6 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
     const float c_tanh = 2.0f * kLog2e * inv_cap;
     const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
+    // A quarter of the cap, as a product of q and k.  (The polynomial's coefficients hold up to the tenth power of
+    // scale / cap, which has to stay within binary32; a NaN among the scores compares false with either bound.)
+    const float near = inv_cap <= 1.0f && inv_cap >= 0x1p-12f ? 0.25f / inv_cap : -1.0f;
     bool ok = true;
     uint32_t s_phase = 0, o_phase = 0;  // of s_full and o_full
     int turn = 0;                       // of the exchange buffers
@@ -424,26 +430,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto first_pass = [&](auto& v, int key0, bool masked) {
         constexpr int N = sizeof(v) / sizeof(v[0]);
         if constexpr (CAP) {
-          // Scores within the cap on either side (all of them, unless the scores are far beyond it) take the
-          // polynomial for tanh; others two special functions each.
+          // Scores within the cap on either side (all of them, unless the scores are far beyond it) take a polynomial
+          // for tanh, in s^2 with the scale and the cap in its coefficients: 4 operations per score within a quarter of
+          // the cap, 7 within the cap.  Others take two special functions each.
           float far = 0.0f;
 #pragma unroll
-          for (int x = 0; x < N; x += 2) far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
-          if (__all_sync(0xFFFFFFFFu, far * inv_cap <= 1.0f)) {
+          for (int x = 0; x < N; x += 2) {
+            far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
+          }
+          const auto polynomial = [&](auto terms, const float* k) {
+            constexpr int T = decltype(terms)::value;
+            uint64_t a[T];
+            float f = c_cap * inv_cap;
+#pragma unroll
+            for (int y = 0; y < T; ++y, f *= inv_cap * inv_cap) a[y] = both(k[y] * f);
 #pragma unroll
             for (int x = 0; x < N; x += 2) {
-              const uint64_t y = mul2(pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), both(inv_cap));
+              const uint64_t y = pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
               const uint64_t u = mul2(y, y);
-              uint64_t t = fma2(u, both(kTanh[5]), both(kTanh[4]));
-              t = fma2(t, u, both(kTanh[3]));
-              t = fma2(t, u, both(kTanh[2]));
-              t = fma2(t, u, both(kTanh[1]));
-              t = fma2(t, u, both(kTanh[0]));
+              uint64_t t = a[T - 1];
+#pragma unroll
+              for (int z = T - 2; z >= 0; --z) t = fma2(t, u, a[z]);
               float a0, a1;
-              unpair(mul2(t, mul2(y, both(c_cap))), a0, a1);
+              unpair(mul2(t, y), a0, a1);
               v[x] = __float_as_uint(a0);
               v[x + 1] = __float_as_uint(a1);
             }
+          };
+          if (__all_sync(0xFFFFFFFFu, far <= near)) {
+            polynomial(std::integral_constant<int, 3>{}, kTanhNear);
+          } else if (__all_sync(0xFFFFFFFFu, far <= 4.0f * near)) {
+            polynomial(std::integral_constant<int, 6>{}, kTanh);
           } else {
 #pragma unroll
             for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
