@@ -48,6 +48,7 @@ inline bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t toke
 }
 
 cudaError_t launch_attention_rows(const AttnParams& p, int head_dim, int sms, cudaStream_t stream);
+double rows_cost(const AttnParams& p, int sms, int* best_splits);
 cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, cudaStream_t stream);
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -73,36 +74,54 @@ __device__ __forceinline__ int doc_start(const int32_t* cu, int d, int docs, int
 // over the documents without a table: document d's slots begin at
 // floor(start_d * per / rows) + d, which leaves room for every document's
 // slots (a document of n rows needs at most floor((s + n)/rows) - floor(s/rows)
-// + 1 of them) and at most one unused slot per document.  slot_doc finds the
-// last document that begins at or before a slot, 32 candidates at a time (one
-// load for up to 32 documents); all lanes of the warp return the same.
-__device__ __forceinline__ int slot_begin(const AttnParams& p, int d, int per, int rows) {
-  return static_cast<int>(static_cast<int64_t>(doc_start(p.cu_q, d, p.docs, p.tokens_q)) * per / rows) + d;
+// + 1 of them) and at most one unused slot per document.
+__device__ __forceinline__ int slot_begin(int start, int d, int per, int rows) {
+  return static_cast<int>(static_cast<int64_t>(start) * per / rows) + d;
 }
 
-__device__ __forceinline__ int slot_doc(const AttnParams& p, int slot, int per, int rows) {
+// The document of a slot, and the slot's first row in it (negative, or past
+// the document's rows, in an unused slot): the last document that begins at
+// or before the slot, 32 candidates at a time.  All lanes of the warp call it
+// and return the same.  Up to 31 documents take one round of loads, a lane
+// each, for everything there is to know.
+__device__ __forceinline__ Doc slot_doc(const AttnParams& p, int slot, int per, int rows, int& row0) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, n = p.docs;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int d = lo + lane * step;
-    const bool before = d < lo + n && slot_begin(p, d, per, rows) <= slot;
-    const int count = max(1, __popc(__ballot_sync(0xFFFFFFFFu, before)));
-    const int skip = (count - 1) * step;
-    lo += skip;
-    n = min(step, n - skip);
-  }
-  return lo;
-}
-
-__device__ __forceinline__ Doc load_doc(const AttnParams& p, int d) {
   Doc r;
-  r.q0 = doc_start(p.cu_q, d, p.docs, p.tokens_q);
-  r.lq = max(0, doc_start(p.cu_q, d + 1, p.docs, p.tokens_q) - r.q0);
-  r.k0 = doc_start(p.cu_k, d, p.docs, p.tokens_k);
-  r.lk = max(0, doc_start(p.cu_k, d + 1, p.docs, p.tokens_k) - r.k0);
+  int d = 0;
+  if (p.docs < 32) {
+    const int q = doc_start(p.cu_q, min(lane, p.docs), p.docs, p.tokens_q);
+    const int k = doc_start(p.cu_k, min(lane, p.docs), p.docs, p.tokens_k);
+    const int prefix = p.prefix != nullptr ? __ldg(p.prefix + min(lane, p.docs - 1)) : 0;
+    const int begin = slot_begin(q, lane, per, rows);
+    d = max(0, __popc(__ballot_sync(0xFFFFFFFFu, lane < p.docs && begin <= slot)) - 1);
+    row0 = (slot - __shfl_sync(0xFFFFFFFFu, begin, d)) * rows;
+    r.q0 = __shfl_sync(0xFFFFFFFFu, q, d);
+    r.lq = __shfl_sync(0xFFFFFFFFu, q, d + 1);
+    r.k0 = __shfl_sync(0xFFFFFFFFu, k, d);
+    r.lk = __shfl_sync(0xFFFFFFFFu, k, d + 1);
+    r.prefix = __shfl_sync(0xFFFFFFFFu, prefix, d);
+  } else {
+    int n = p.docs;
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int at = d + lane * step;
+      const bool before =
+          at < d + n && slot_begin(doc_start(p.cu_q, at, p.docs, p.tokens_q), at, per, rows) <= slot;
+      const int skip = (max(1, __popc(__ballot_sync(0xFFFFFFFFu, before))) - 1) * step;
+      d += skip;
+      n = min(step, n - skip);
+    }
+    r.q0 = doc_start(p.cu_q, d, p.docs, p.tokens_q);
+    r.lq = doc_start(p.cu_q, d + 1, p.docs, p.tokens_q);
+    r.k0 = doc_start(p.cu_k, d, p.docs, p.tokens_k);
+    r.lk = doc_start(p.cu_k, d + 1, p.docs, p.tokens_k);
+    r.prefix = p.prefix != nullptr ? __ldg(p.prefix + d) : 0;
+    row0 = (slot - slot_begin(r.q0, d, per, rows)) * rows;
+  }
+  r.lq = max(0, r.lq - r.q0);
+  r.lk = max(0, r.lk - r.k0);
   r.shift = r.lk - r.lq;
-  r.prefix = p.prefix != nullptr ? min(max(__ldg(p.prefix + d), 0), r.lk) : 0;
+  r.prefix = min(max(r.prefix, 0), r.lk);
   return r;
 }
 

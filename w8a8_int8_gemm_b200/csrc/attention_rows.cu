@@ -37,7 +37,7 @@ constexpr int kThreads = 32 * kWarps + 32;
 constexpr int kTileK = 16 * kWarps;  // keys of a tile
 constexpr int kStages = 3;
 constexpr int kRows = 16;
-constexpr int kFill = 4;              // CTAs per SM that the splits aim at
+constexpr int kMaxSplits = 8;
 constexpr int kBlock = kTileK * 128;  // bytes of 64 values of a tile's keys
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -93,10 +93,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                           const AttnParams p, const int splits, int* err) {
   constexpr int kBlocks = D / 64;
   constexpr int kStage = stage_bytes<D>();
-  static_assert(kWarps * kRows * D * 4 <= kStages * kStage, "partial results fit the ring");
+  constexpr int kPartRow = D + 8;  // floats of a row of partial results, padded against bank conflicts
+  static_assert(kWarps * kRows * kPartRow * 4 <= kStages * kStage, "partial results fit the ring");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* part = reinterpret_cast<float*>(smem);  // [warp][row][D] scaled to the CTA's maximum; [0] becomes their sum
+  // [warp][row][kPartRow], scaled to the CTA's maximum; [0] becomes their sum
+  float* part = reinterpret_cast<float*>(smem);
   __shared__ float sh_m[kWarps][kRows], sh_l[kWarps][kRows], cta_m[kRows], cta_l[kRows];
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ int abort_word;
@@ -118,9 +120,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     abort_word = 0;
     fence_mbar_init();
   }
-  const int d = slot_doc(p, slot, p.group, kRows);
-  const Doc doc = load_doc(p, d);
-  const int row0 = (slot - slot_begin(p, d, p.group, kRows)) * kRows;
+  int row0;
+  const Doc doc = slot_doc(p, slot, p.group, kRows, row0);
   const int rows = min(kRows, doc.lq * p.group - row0);  // rows of this slot
   if (rows <= 0 || row0 < 0) return;  // an unused slot (the whole cluster's)
   // Keys any row of the slot sees (limits grow with the token), and this CTA's tiles of them: every splits-th.
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const float f = ex2(m[h] - (top == -INFINITY ? 0.0f : top));
       if (t == 0) sh_l[warp][g + 8 * h] = l[h] * f;
       if (warp == 0 && t == 0) cta_m[g + 8 * h] = top;
-      float* to = part + (warp * kRows + g + 8 * h) * D + 2 * t;
+      float* to = part + (warp * kRows + g + 8 * h) * kPartRow + 2 * t;
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) {
         *reinterpret_cast<float2*>(to + 8 * n) = make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
@@ -304,11 +305,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < kRows * D; e += kThreads) {
-    float sum = 0.0f;
+  for (int e = threadIdx.x; e < kRows * D / 4; e += kThreads) {
+    float4* at = reinterpret_cast<float4*>(part + e / (D / 4) * kPartRow + e % (D / 4) * 4);
+    float4 sum = *at;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += part[w * kRows * D + e];
-    part[e] = sum;
+    for (int w = 1; w < kWarps; ++w) {
+      const float4 x = at[w * kRows * kPartRow / 4];
+      sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+    }
+    *at = sum;
   }
   if (threadIdx.x < kRows) {
     float sum = 0.0f;
@@ -328,16 +333,31 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint32_t l_addr = smem_u32(&cta_l[0]);
   for (int e = 2 * (split * kThreads + static_cast<int>(threadIdx.x)); e < rows * D; e += 2 * splits * kThreads) {
     const int r = e / D, col = e % D;
-    float top = -INFINITY;
-    for (int c = 0; c < splits; ++c) top = fmaxf(top, ld_cluster_f32(map_to_cta(m_addr + 4 * r, c)));
+    // (unrolled, so that the remote loads overlap)
+    float cm[kMaxSplits], cl[kMaxSplits], c0[kMaxSplits], c1[kMaxSplits];
+#pragma unroll
+    for (int c = 0; c < kMaxSplits; ++c) {
+      cm[c] = -INFINITY;
+      cl[c] = c0[c] = c1[c] = 0.0f;
+      if (c < splits) {
+        cm[c] = ld_cluster_f32(map_to_cta(m_addr + 4 * r, c));
+        cl[c] = ld_cluster_f32(map_to_cta(l_addr + 4 * r, c));
+        const uint32_t a = map_to_cta(part_addr + 4 * (r * kPartRow + col), c);
+        c0[c] = ld_cluster_f32(a);
+        c1[c] = ld_cluster_f32(a + 4);
+      }
+    }
+    float top = cm[0];
+#pragma unroll
+    for (int c = 1; c < kMaxSplits; ++c) top = fmaxf(top, cm[c]);
     const float from = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f, x0 = 0.0f, x1 = 0.0f;
-    for (int c = 0; c < splits; ++c) {
-      const float f = ex2(ld_cluster_f32(map_to_cta(m_addr + 4 * r, c)) - from);
-      const uint32_t a = map_to_cta(part_addr + 4 * e, c);
-      sum += f * ld_cluster_f32(map_to_cta(l_addr + 4 * r, c));
-      x0 += f * ld_cluster_f32(a);
-      x1 += f * ld_cluster_f32(a + 4);
+#pragma unroll
+    for (int c = 0; c < kMaxSplits; ++c) {
+      const float f = ex2(cm[c] - from);
+      sum = fmaf(f, cl[c], sum);
+      x0 = fmaf(f, c0[c], x0);
+      x1 = fmaf(f, c1[c], x1);
     }
     const int i = (row0 + r) / p.group;
     const int head = kv_head * p.group + (row0 + r) % p.group;
@@ -393,13 +413,29 @@ cudaError_t launch(const AttnParams& p, int splits, cudaStream_t stream) {
 
 }  // namespace
 
+// What the row kernel takes for documents of the average length, in us, and the CTAs per slot that take least.  A CTA
+// needs about 5 us beside its tiles and 1 us a tile of 64 keys, and two share an SM.  (Measured with 1, 2, 4 and 8
+// CTAs a slot: 16 sequences of 12 000 keys, 8 key/value heads: 149, 79, 86, 101 us; 16 of 2 000: 24, 19, 25, 36; 64 of
+// 512, 4 rows each: 36, 50, 79, 149; one of 2304, 24 heads: 25, 16, 11, 11.)
+double rows_cost(const AttnParams& p, int sms, int* best_splits) {
+  const int64_t rows = (static_cast<int64_t>(p.tokens_q) * p.group + p.docs - 1) / p.docs;
+  const int64_t units = (rows + kRows - 1) / kRows * p.docs * p.heads_k;
+  const int64_t tiles = (p.tokens_k / p.docs + kTileK - 1) / kTileK;
+  double best = 0.0;
+  for (int splits = 1; splits <= kMaxSplits; splits *= 2) {
+    const int64_t rounds = (units * splits + 2 * sms - 1) / (2 * sms);
+    const double cost = static_cast<double>(rounds) * (5.0 + static_cast<double>((tiles + splits - 1) / splits));
+    if (splits == 1 || cost < best) {
+      best = cost;
+      *best_splits = splits;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_attention_rows(const AttnParams& p, int head_dim, int sms, cudaStream_t stream) {
-  // CTAs per slot: enough to fill every SM twice, as long as a CTA keeps two tiles.
-  const int64_t rows_per_doc = (static_cast<int64_t>(p.tokens_q) * p.group + p.docs - 1) / p.docs;
-  const int64_t units = (rows_per_doc + kRows - 1) / kRows * p.docs * p.heads_k;
-  const int64_t keys_per_doc = p.tokens_k / p.docs;
   int splits = 1;
-  while (splits < 8 && units * splits < kFill * sms && keys_per_doc >= 2 * splits * 2 * kTileK) splits *= 2;
+  rows_cost(p, sms, &splits);
   const bool cap = p.cap > 0.0f, bias = p.slopes != nullptr;
   if (head_dim == 64) {
     if (cap) return bias ? launch<64, true, true>(p, splits, stream) : launch<64, true, false>(p, splits, stream);

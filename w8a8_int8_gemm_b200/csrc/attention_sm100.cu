@@ -157,9 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     it.head = p.causal ? x % p.heads_q : x / slots;
     const int slot = p.causal ? slots - 1 - x / p.heads_q : x % slots;
-    const int d = slot_doc(p, slot, 1, kTileQ);
-    it.doc = load_doc(p, d);
-    it.row0 = (slot - slot_begin(p, d, 1, kTileQ)) * kTileQ;
+    it.doc = slot_doc(p, slot, 1, kTileQ, it.row0);
     it.rows = it.row0 < 0 ? 0 : min(kTileQ, it.doc.lq - it.row0);
     const auto key_tiles = [&](int s) {
       const int n = min(kSub, it.rows - s * kSub);
