@@ -439,8 +439,8 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  * (the last query stands at the last key, as in a cache; a prefix longer than
  * the document is the whole document).  A query that sees no key gets 0 and an
  * lse of -inf.  Scores, maxima, sums and weighted sums are binary32; the
- * weights exp(s - max) enter the product with v in bf16 (in two bf16 parts
- * where queries are few); out is rounded once.
+ * weights exp(s - max) enter the product with v in bf16 (in two bf16 parts in
+ * the kernel for few queries); out is rounded once.
  *
  *   q, out   bf16 [tokens_q, heads_q, head_dim];  k, v  bf16 [tokens_k, heads_k,
  *            head_dim]: the last dimension contiguous, ld* the stride of a
@@ -464,6 +464,12 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  * tokens up to 2^30; scale > 0; 0 <= cap <= 1e6 (0: no cap; a cap adds an
  * error of 1e-6 * cap to a score).  tokens_q == 0 launches nothing.
  */
+/* Two kernels compute it, for any shape: one reads K and V once for 16 (query,
+ * head) rows and splits the keys (single tokens, short documents), one takes
+ * tiles of 256 queries on the tensor cores.  AUTO chooses by an estimate of
+ * their times for documents of the average length. */
+enum { W8A8_ATTENTION_AUTO = 0, W8A8_ATTENTION_ROWS = 1, W8A8_ATTENTION_TILES = 2 };
+
 typedef struct {
     const void* q;
     const void* k;
@@ -478,6 +484,7 @@ typedef struct {
     int64_t ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso;
     int32_t docs, heads_q, heads_k, head_dim;
     int32_t causal;           /* 0 or 1 */
+    int32_t kernel;           /* W8A8_ATTENTION_AUTO, or a kernel by name for sweeps and tests */
     float scale;
     float cap;
 } w8a8_attention_desc;

@@ -80,14 +80,17 @@ def check(out, lse, q, k, v, cu_q, cu_k, scale, cap=0.0, causal=False, prefix=No
         assert bool((off <= tol)[~none].all()), f"document {d}: lse off by {float((off / tol)[~none].max())} tolerances"
 
 
-def case(w8, docs, Hq, Hk, D, seed=0, r=2.0 ** -8, std=1.0, **how):
+KERNELS = [0, 1, 2]  # chosen, for few queries, for many
+
+
+def case(w8, docs, Hq, Hk, D, seed=0, r=2.0 ** -8, std=1.0, kernel=0, **how):
     lq, lk = [x for x, _ in docs], [y for _, y in docs]
     q = tensor(sum(lq), Hq, D, seed=seed + 1, std=std)
     k = tensor(sum(lk), Hk, D, seed=seed + 2, std=std)
     v = tensor(sum(lk), Hk, D, seed=seed + 3)
     cu_q, cu_k = starts(lq), starts(lk)
     lse = torch.full((sum(lq), Hq), 9.0, device=DEV)
-    out = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, lse=lse, **how)
+    out = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, lse=lse, kernel=kernel, **how)
     torch.cuda.synchronize()
     assert w8.w8a8_read_device_error() == 0
     check(out, lse, q, k, v, cu_q, cu_k, how.pop("scale", D ** -0.5), r=r, **how)
@@ -109,7 +112,8 @@ DOCS = {
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("how", ["plain", "causal", "prefix", "cap", "bias", "all"])
 @pytest.mark.parametrize("docs", list(DOCS))
-def test_masks_and_lengths(w8, docs, how, D):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_masks_and_lengths(w8, kernel, docs, how, D):
     shapes = DOCS[docs]
     Hq, Hk = {"plain": (3, 3), "causal": (6, 2), "prefix": (4, 1), "cap": (2, 2), "bias": (8, 4), "all": (5, 1)}[how]
     args = {}
@@ -121,27 +125,30 @@ def test_masks_and_lengths(w8, docs, how, D):
         args["cap"] = 2.5 if how == "cap" else 30.0
     if how in ("bias", "all"):
         args["slopes"] = 2.0 ** -torch.arange(1, Hq + 1, device=DEV, dtype=torch.float32)
-    case(w8, shapes, Hq, Hk, D, seed=len(docs), **args)
+    case(w8, shapes, Hq, Hk, D, seed=len(docs), kernel=kernel, **args)
 
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G", [1, 3, 8, 16, 40])
 def test_shared_heads_single_tokens(w8, G, D):
-    """One to four tokens per sequence over ragged caches; weights in two parts (r = 2^-16)."""
-    case(w8, [(1, 700), (1, 5000), (1, 1), (1, 15), (1, 17), (1, 0), (1, 2049)], 2 * G, 2, D, r=2.0 ** -15, causal=True)
-    if G <= 3:
-        case(w8, [(4, 700), (3, 33), (2, 2), (4, 1025)], 2 * G, 2, D, r=2.0 ** -15, causal=True)
+    """One to four tokens per sequence over ragged caches, in the row kernel: weights in two parts (r = 2^-16)."""
+    how = dict(r=2.0 ** -16, causal=True, kernel=w8.ATTENTION_ROWS)
+    case(w8, [(1, 700), (1, 5000), (1, 1), (1, 15), (1, 17), (1, 0), (1, 2049)], 2 * G, 2, D, **how)
+    case(w8, [(4, 700), (3, 33), (2, 2), (4, 1025)], 2 * G, 2, D, **how)
+    case(w8, [(1, 1000 * i + 1) for i in range(40)], 2 * G, 2, D, causal=True)  # the chosen kernel
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("scale,std", [(1.0, 2.0), (0.01, 1.0), (30.0, 1.0)])
-def test_sharp_and_flat_weights(w8, scale, std):
-    case(w8, [(300, 300), (1, 300)], 2, 2, 64, scale=scale, std=std)
-    case(w8, [(140, 400), (3, 300)], 2, 1, 128, scale=scale, std=std, causal=True)
+def test_sharp_and_flat_weights(w8, scale, std, kernel):
+    case(w8, [(300, 300), (1, 300)], 2, 2, 64, scale=scale, std=std, kernel=kernel)
+    case(w8, [(140, 400), (3, 300)], 2, 1, 128, scale=scale, std=std, causal=True, kernel=kernel)
 
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("cap", [1e-3, 0.3, 4.0, 50.0, 700.0, 1e5])
-def test_cap_over_its_range(w8, cap, D):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_cap_over_its_range(w8, kernel, cap, D):
     """Scores far inside the cap, around it and far beyond it, in the same tile and in tiles of their own."""
     for Lq in (2, 150):
         q, k, v = tensor(Lq, 2, D), tensor(450, 2, D, seed=2), tensor(450, 2, D, seed=3)
@@ -149,11 +156,12 @@ def test_cap_over_its_range(w8, cap, D):
         k[:130] *= 0.05
         k[300:] *= 4.0
         lse = torch.empty(Lq, 2, device=DEV)
-        out = w8.w8a8_attention(q, k, v, cap=cap, lse=lse)
+        out = w8.w8a8_attention(q, k, v, cap=cap, lse=lse, kernel=kernel)
         check(out, lse, q, k, v, [0, Lq], [0, 450], D ** -0.5, cap=cap)
 
 
-def test_scores_that_climb(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scores_that_climb(w8, kernel):
     """The running maximum grows with every tile of keys, by more and less than a power of 2^8 at a time."""
     for step in (0.02, 0.5):
         for Lq in (1, 200):
@@ -165,11 +173,12 @@ def test_scores_that_climb(w8):
             v = tensor(L, 1, D, seed=5)
             lse = torch.empty(Lq, 1, device=DEV)
             for kk in (k, k.flip(0)):
-                out = w8.w8a8_attention(q, kk, v, scale=1.0, lse=lse)
+                out = w8.w8a8_attention(q, kk, v, scale=1.0, lse=lse, kernel=kernel)
                 check(out, lse, q, kk, v, [0, Lq], [0, L], 1.0)
 
 
-def test_views_gaps_and_garbage(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_views_gaps_and_garbage(w8, kernel):
     """Strided views of one buffer; NaN and infinities in every token outside the documents; rows of out and lse
     outside them stay as they were."""
     for lens in ([(1, 130), (1, 257), (1, 3)], [(150, 150), (70, 70), (300, 300)]):
@@ -186,34 +195,36 @@ def test_views_gaps_and_garbage(w8):
         q[:fq], q[int(cu_q[-1]):] = float("nan"), float("inf")
         buf = torch.full((Tq, Hq + 2, D), 3.0, dtype=torch.bfloat16, device=DEV)
         lse = torch.full((Tq, Hq), 5.0, device=DEV)
-        w8.w8a8_attention(q, k, v, causal=True, cu_q=cu_q, cu_k=cu_k, out=buf[:, 1:-1], lse=lse)
+        w8.w8a8_attention(q, k, v, causal=True, cu_q=cu_q, cu_k=cu_k, out=buf[:, 1:-1], lse=lse, kernel=kernel)
         check(buf[:, 1:-1], lse, q, k, v, cu_q, cu_k, D ** -0.5, causal=True)
         assert bool((buf[:, 0] == 3).all()) and bool((buf[:, -1] == 3).all())
         for t in (slice(0, fq), slice(int(cu_q[-1]), Tq)):
             assert bool((buf[t] == 3).all()) and bool((lse[t] == 5).all())
 
 
-def test_a_neighbour_full_of_nan(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_neighbour_full_of_nan(w8, kernel):
     """NaN in one document's keys and values stays in that document."""
     for lens in ([(1, 130), (1, 70), (1, 200)], [(130, 130), (70, 70), (200, 200)]):
         lq, lk = [a for a, _ in lens], [b for _, b in lens]
         q, k, v = tensor(sum(lq), 2, 64), tensor(sum(lk), 2, 64, seed=2), tensor(sum(lk), 2, 64, seed=3)
         cu_q, cu_k = starts(lq), starts(lk)
-        clean = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k)
+        clean = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, kernel=kernel)
         k[int(cu_k[1]):int(cu_k[2])] = float("nan")
         v[int(cu_k[1]):int(cu_k[2])] = float("nan")
-        out = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k)
+        out = w8.w8a8_attention(q, k, v, cu_q=cu_q, cu_k=cu_k, kernel=kernel)
         a, b = int(cu_q[1]), int(cu_q[2])
         assert torch.equal(out[:a], clean[:a]) and torch.equal(out[b:], clean[b:])
         assert bool(torch.isnan(out[a:b]).all())
 
 
-def test_hidden_keys_may_hold_anything(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_hidden_keys_may_hold_anything(w8, kernel):
     """Keys past every query's limit: NaN scores and values that nothing sees."""
     for Lq, Lk in ((1, 300), (150, 150)):
         q, k, v = tensor(Lq, 2, 128), tensor(Lk, 2, 128, seed=2), tensor(Lk, 2, 128, seed=3)
         k[100] = float("nan")  # a NaN key that is seen makes its queries NaN
-        out = w8.w8a8_attention(q, k, v, causal=True)
+        out = w8.w8a8_attention(q, k, v, causal=True, kernel=kernel)
         sees = torch.arange(Lq, device=DEV) + Lk - Lq >= 100
         assert bool(torch.isnan(out[sees]).all()) and bool(torch.isfinite(out[~sees]).all())
 
@@ -225,22 +236,24 @@ def test_equal_parts_without_starts(w8):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("most", [3, 40])
-def test_thousands_of_documents(w8, most):
+def test_thousands_of_documents(w8, most, kernel):
     n = 2500
     lens = [1 + (7 * i) % most for i in range(n)]
     q, k, v = tensor(sum(lens), 2, 64), tensor(sum(lens), 1, 64, seed=2), tensor(sum(lens), 1, 64, seed=3)
     cu = starts(lens)
     lse = torch.empty(sum(lens), 2, device=DEV)
-    out = w8.w8a8_attention(q, k, v, cu_q=cu, cu_k=cu, causal=True, lse=lse)
+    out = w8.w8a8_attention(q, k, v, cu_q=cu, cu_k=cu, causal=True, lse=lse, kernel=kernel)
     at = list(range(0, n, 97)) + [n - 2, n - 1]
     for d in at:
         a, b = int(cu[d]), int(cu[d + 1])
         check(out[a:b], lse[a:b], q[a:b], k[a:b], v[a:b], [0, b - a], [0, b - a], 64 ** -0.5, causal=True)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("Lq", [1, 140])
-def test_offsets_beyond_32_bits(w8, Lq):
+def test_offsets_beyond_32_bits(w8, Lq, kernel):
     """A cache whose token stride puts keys past 2^32 elements."""
     L, ld = 300, 2 ** 24 + 64
     buf = torch.empty((L - 1) * ld + 192, dtype=torch.bfloat16, device=DEV)
@@ -249,16 +262,17 @@ def test_offsets_beyond_32_bits(w8, Lq):
     v.copy_(tensor(L, 1, 64, seed=3))
     q = tensor(Lq, 2, 64)
     lse = torch.empty(Lq, 2, device=DEV)
-    out = w8.w8a8_attention(q, k, v, lse=lse)
+    out = w8.w8a8_attention(q, k, v, lse=lse, kernel=kernel)
     check(out, lse, q, k, v, [0, Lq], [0, L], 64 ** -0.5)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("docs", [[(1, 3000), (1, 100)], [(300, 300), (77, 200)]])
-def test_streams_graphs_and_repeats(w8, docs):
+def test_streams_graphs_and_repeats(w8, docs, kernel):
     lq, lk = [a for a, _ in docs], [b for _, b in docs]
     q, k, v = tensor(sum(lq), 4, 128), tensor(sum(lk), 2, 128, seed=2), tensor(sum(lk), 2, 128, seed=3)
     cu_q, cu_k = starts(lq), starts(lk)
-    how = dict(causal=True, cu_q=cu_q, cu_k=cu_k)
+    how = dict(causal=True, cu_q=cu_q, cu_k=cu_k, kernel=kernel)
     want = w8.w8a8_attention(q, k, v, **how)
     for _ in range(3):
         assert torch.equal(w8.w8a8_attention(q, k, v, **how), want)   # the same bits every time
@@ -280,23 +294,26 @@ def test_streams_graphs_and_repeats(w8, docs):
     assert torch.equal(o, w8.w8a8_attention(q, k, v, **how))
 
 
-def test_no_queries_and_no_keys(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_no_queries_and_no_keys(w8, kernel):
     k = tensor(5, 2, 64)
     assert w8.w8a8_attention(k[:0], k, k).shape == (0, 2, 64)
     lse = torch.zeros(5, 2, device=DEV)
     for q in (k, tensor(200, 2, 64)):
         lse = torch.zeros(q.shape[0], 2, device=DEV)
-        out = w8.w8a8_attention(q, k[:0], k[:0], lse=lse)
+        out = w8.w8a8_attention(q, k[:0], k[:0], lse=lse, kernel=kernel)
         assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
 
-def test_starts_that_decrease_stay_in_bounds(w8):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_starts_that_decrease_stay_in_bounds(w8, kernel):
     """Starts out of order or out of range give some rows or none, inside the arrays they are given."""
     q, k = tensor(64, 2, 64), tensor(64, 2, 64, seed=2)
     buf = torch.full((66, 2, 64), 3.0, dtype=torch.bfloat16, device=DEV)
     for cu in ([0, 60, 20, 64], [-5, 30, 90, 10 ** 9], [64, 32, 16, 0], [2 ** 31 - 1, -2 ** 31, 5, 7]):
         c = torch.tensor(cu, dtype=torch.int32, device=DEV)
-        w8.w8a8_attention(q, k, k, cu_q=c, cu_k=c.flip(0).contiguous(), out=buf[1:-1], causal=True)
+        w8.w8a8_attention(q, k, k, cu_q=c, cu_k=c.flip(0).contiguous(), out=buf[1:-1], causal=True,
+                          kernel=kernel)
         torch.cuda.synchronize()
         assert bool((buf[0] == 3).all()) and bool((buf[-1] == 3).all())
     assert w8.w8a8_read_device_error() == 0
@@ -320,7 +337,7 @@ def test_refusals(w8):
     with pytest.raises(ValueError):
         w8.w8a8_attention(q, k, k, slopes=torch.ones(2, device=DEV))
     for bad in (dict(docs=3), dict(cap=-1.0), dict(scale=0.0), dict(scale=float("nan")), dict(cap=float("inf")),
-                dict(prefix=torch.zeros(1, dtype=torch.int32, device=DEV))):
+                dict(prefix=torch.zeros(1, dtype=torch.int32, device=DEV)), dict(kernel=3)):
         with pytest.raises(w8.W8A8Error) as e:
             w8.w8a8_attention(q, k, k, **bad)
         assert e.value.status == 1

@@ -93,7 +93,7 @@ def attention(w8, **change):
     (dict(tokens_q=-1), 1), (dict(tokens_k=-1), 1), (dict(tokens_q=2 ** 30 + 1), 1), (dict(docs=0), 1),
     (dict(docs=2 ** 24 + 1), 1), (dict(heads_k=0), 1), (dict(heads_q=1, heads_k=2), 1), (dict(heads_q=3, heads_k=2), 1),
     (dict(heads_q=65537), 1), (dict(head_dim=96), 1), (dict(head_dim=256), 1), (dict(cu_q=None, tokens_q=5), 1),
-    (dict(cu_k=None, tokens_k=7), 1), (dict(causal=2), 1), (dict(prefix=A), 1), (dict(scale=0.0), 1),
+    (dict(cu_k=None, tokens_k=7), 1), (dict(causal=2), 1), (dict(kernel=3), 1), (dict(kernel=-1), 1), (dict(prefix=A), 1), (dict(scale=0.0), 1),
     (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(cap=-1.0), 1),
     (dict(cap=float("nan")), 1), (dict(cap=2e6), 1), (dict(q=None), 1), (dict(v=None), 1), (dict(out=None), 1),
     (dict(ldq=32), 1), (dict(ldk=0), 1), (dict(hsq=0), 1), (dict(ldo=64), 1), (dict(hso=8), 1), (dict(ldv=2 ** 31), 1),

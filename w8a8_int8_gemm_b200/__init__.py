@@ -34,7 +34,8 @@ __all__ = [
     "w8a8_quantize_act_gelu", "w8a8_gelu", "w8a8_linear_gelu", "ACT_NONE", "ACT_GELU", "ACT_SILU",
     "w8a8_gemm_glu", "w8a8_gemm_glu_ex", "w8a8_gemm_glu_fp8", "w8a8_gemm_glu_fp8_ex", "w8a8_linear_glu",
     "w8a8_linear_glu_fp8",
-    "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS", "w8a8_attention",
+    "w8a8_qk_norm_rope", "ROPE_HALVES", "ROPE_PAIRS",
+    "w8a8_attention", "ATTENTION_AUTO", "ATTENTION_ROWS", "ATTENTION_TILES",
     "LinearDesc", "Chain", "linear_layer", "w8a8_chain_create", "w8a8_chain_launch", "w8a8_chain_layers",
     "w8a8_chain_destroy",
     "w8a8_select_config",
@@ -52,6 +53,9 @@ ACT_GELU = 1   # W8A8_ACT_GELU
 ACT_SILU = 2   # W8A8_ACT_SILU
 ROPE_HALVES = 0  # W8A8_ROPE_HALVES
 ROPE_PAIRS = 1   # W8A8_ROPE_PAIRS
+ATTENTION_AUTO = 0   # W8A8_ATTENTION_AUTO
+ATTENTION_ROWS = 1   # W8A8_ATTENTION_ROWS
+ATTENTION_TILES = 2  # W8A8_ATTENTION_TILES
 
 
 class W8A8Error(RuntimeError):
@@ -90,7 +94,7 @@ class QkDesc(ctypes.Structure):
 # The descriptors' layouts for struct, which packs one in a quarter of the time that it takes to fill a ctypes
 # structure (a null pointer is 0).
 _QK_DESC = struct.Struct("@9P10q5if0q")
-_ATTENTION_DESC = struct.Struct("@9P10q5i2f0q")
+_ATTENTION_DESC = struct.Struct("@9P10q6i2f0q")
 
 
 class AttentionDesc(ctypes.Structure):
@@ -98,7 +102,7 @@ class AttentionDesc(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "cu_q", "cu_k", "prefix", "slopes")]
                 + [(n, ctypes.c_int64) for n in ("tokens_q", "tokens_k", "ldq", "hsq", "ldk", "hsk", "ldv", "hsv",
                                                  "ldo", "hso")]
-                + [(n, ctypes.c_int32) for n in ("docs", "heads_q", "heads_k", "head_dim", "causal")]
+                + [(n, ctypes.c_int32) for n in ("docs", "heads_q", "heads_k", "head_dim", "causal", "kernel")]
                 + [("scale", ctypes.c_float), ("cap", ctypes.c_float)])
 
 
@@ -768,15 +772,16 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
 
 
 def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal: bool = False, cu_q=None, cu_k=None,
-                   docs: int | None = None, prefix=None, slopes=None, out=None, lse=None, stream=None):
+                   docs: int | None = None, prefix=None, slopes=None, out=None, lse=None,
+                   kernel: int = ATTENTION_AUTO, stream=None):
     """Softmax attention over packed documents: out bf16 [Tq, Hq, D] from q [Tq, Hq, D] and k, v [Tk, Hk, D]
     (Hq a multiple of Hk, D 64 or 128, strided views allowed).
 
     cu_q, cu_k: int32 [docs + 1] starts of the documents in each stream; without them docs (default 1) equal
     parts.  scale defaults to D ** -0.5; cap > 0 caps the scores by cap * tanh(s / cap); causal with prefix
     (int32 [docs]) shows each query the keys up to its own place and the document's prefix; slopes (fp32 [Hq])
-    subtracts slope * distance.  lse: fp32 [Tq, Hq] tensor that receives the scores' log-sum-exp.  See
-    include/w8a8.h."""
+    subtracts slope * distance.  lse: fp32 [Tq, Hq] tensor that receives the scores' log-sum-exp.  kernel:
+    ATTENTION_ROWS or ATTENTION_TILES by name, for sweeps and tests.  See include/w8a8.h."""
     ldq, hsq = _heads(q, "q")
     Tq, Hq, D = q.shape
     ldk, hsk = _heads(k, "k", D)
@@ -801,7 +806,7 @@ def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal
     dev = _one_device(q, k, v, cu_q, cu_k, prefix, slopes, out, lse)
     desc = _ATTENTION_DESC.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse) or 0,
                                 _ptr(cu_q) or 0, _ptr(cu_k) or 0, _ptr(prefix) or 0, _ptr(slopes) or 0, Tq, Tk, ldq,
-                                hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D, 1 if causal else 0,
+                                hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D, 1 if causal else 0, kernel,
                                 float(D ** -0.5 if scale is None else scale), float(cap))
     _check(_call(dev, _lib.w8a8_attention, desc, _stream(stream, dev)), "w8a8_attention")
     return out

@@ -39,6 +39,7 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
     return W8A8_ERR_INVALID_ARG;
   }
   if (a->causal != 0 && a->causal != 1) return W8A8_ERR_INVALID_ARG;
+  if (a->kernel < W8A8_ATTENTION_AUTO || a->kernel > W8A8_ATTENTION_TILES) return W8A8_ERR_INVALID_ARG;
   if (a->prefix != nullptr && !a->causal) return W8A8_ERR_INVALID_ARG;
   if (!(a->scale > 0.0f) || a->scale > 3.0e38f || !(a->cap >= 0.0f) || a->cap > 1.0e6f) return W8A8_ERR_INVALID_ARG;
   if (a->tokens_q == 0) return W8A8_OK;
@@ -102,6 +103,7 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
   const int64_t items = (queries + 255) / 256 * a->docs * a->heads_q;
   const double tiles = static_cast<double>(a->tokens_k / a->docs) / 80.0;
   const double by_tiles = static_cast<double>((items + sms - 1) / sms) * (5.0 + tiles * (queries > 128 ? 1.1 : 0.9));
-  if (by_rows <= by_tiles) return status_of(launch_attention_rows(p, a->head_dim, sms, s));
+  const bool by_row_kernel = a->kernel == W8A8_ATTENTION_AUTO ? by_rows <= by_tiles : a->kernel == W8A8_ATTENTION_ROWS;
+  if (by_row_kernel) return status_of(launch_attention_rows(p, a->head_dim, sms, s));
   return status_of(launch_attention_tiles(p, a->head_dim, s));
 }
