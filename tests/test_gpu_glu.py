@@ -192,6 +192,25 @@ def test_captured_and_other_stream(w8):
     check(w8, out, ws, wq, sa, sw, bias, w8.ACT_SILU)
 
 
+def test_workspace_of_a_call_on_another_stream(w8):
+    """A workspace allocated inside the call belongs to the call's stream: the current stream may not get its memory
+    back while the other stream still has the call ahead of it."""
+    x, wq, sw, bias = inputs(w8, 512, 256, 1024, False, seed=12)
+    want = w8.w8a8_linear_glu(x, wq, sw, bias)
+    busy = torch.randn(8192, 8192, device=DEV).bfloat16()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for as_number in (False, True):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                busy = (busy @ busy) * 1e-3
+        out = w8.w8a8_linear_glu(x, wq, sw, bias, stream=s.cuda_stream if as_number else s)
+        for n in (512 * 1024, 512 * 1024 + 2048, 2048, 512 * 256 * 2):  # the sizes that could be handed out again
+            torch.full((n,), 77, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_empty_and_refusals(w8):
     x, wq, sw, bias = inputs(w8, 4, 16, 32, False)
     assert w8.w8a8_linear_glu(x[:0], wq, sw, bias).shape == (0, 16)

@@ -596,6 +596,17 @@ def w8a8_linear_gelu(h, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a
 # ------------------------------------------------- the gated linear layer
 
 
+def _empty(like: torch.Tensor, shape: tuple, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A new tensor beside `like` that belongs to the stream of the call: memory of another stream could be handed
+    out again by that stream before this one's kernels are done with it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _gemm_glu(fn, what, code, xq, wq, scale_a, scale_w, bias, out, act, config, stream):
     _need(xq, "xq", code, 2)
     M, K = xq.shape
@@ -603,8 +614,9 @@ def _gemm_glu(fn, what, code, xq, wq, scale_a, scale_w, bias, out, act, config, 
     N = _glu_weight(wq, code, K, scale_w, bias)
     _need_contig(scale_a, "scale_a", torch.float32, (M,))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
-    _need_contig(out, "out", torch.bfloat16, (M, N))
+        out = _empty(xq, (M, N), torch.bfloat16, stream)
+    else:
+        _need_contig(out, "out", torch.bfloat16, (M, N))
     dev = _one_device(xq, wq, scale_a, scale_w, bias, out)
     c = _cfg(config)
     _check(_call(dev, fn, _ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K, int(act),
@@ -659,20 +671,25 @@ def _linear_glu(fn, what, code, x, wq, scale_w, bias, out, act, ws_xq, ws_scale_
     _need_contig(x, "x", torch.bfloat16, (M, K))
     N = _glu_weight(wq, code, K, scale_w, bias)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(x, (M, N), torch.bfloat16, stream)
     else:
         _need_contig(out, "out", torch.bfloat16, (M, N))
-    if ws_xq is None:
-        ws_xq = torch.empty((M, K), dtype=code, device=x.device)
+    if ws_xq is None and ws_scale_a is None:
+        # one allocation for both: the codes, then the scales (16-byte aligned)
+        scales = (M * K + 15) // 16 * 16
+        ws = _empty(x, (scales + 4 * M,), torch.uint8, stream)
+        xq_ptr = ws.data_ptr()
+        sa_ptr = xq_ptr + scales
+        dev = _one_device(x, wq, scale_w, bias, out)
     else:
+        ws_xq = _empty(x, (M, K), code, stream) if ws_xq is None else ws_xq
+        ws_scale_a = _empty(x, (M,), torch.float32, stream) if ws_scale_a is None else ws_scale_a
         _need_contig(ws_xq, "ws_xq", code, (M, K))
-    if ws_scale_a is None:
-        ws_scale_a = torch.empty((M,), dtype=torch.float32, device=x.device)
-    else:
         _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
-    dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
-    _check(_call(dev, fn, _ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq), _ptr(ws_scale_a), M, N,
-                 K, int(act), _stream(stream, dev)), what)
+        xq_ptr, sa_ptr = ws_xq.data_ptr(), ws_scale_a.data_ptr()
+        dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
+    _check(_call(dev, fn, x.data_ptr(), wq.data_ptr(), scale_w.data_ptr(), _ptr(bias), out.data_ptr(), xq_ptr, sa_ptr, M,
+                 N, K, int(act), _stream(stream, dev)), what)
     return out
 
 
@@ -709,11 +726,15 @@ def _heads(t: torch.Tensor, name: str, dim: int | None = None) -> tuple:
     return (ld if rows > 1 else max(1, heads) * hs), hs
 
 
-def _heads_out(t, name: str, like: torch.Tensor) -> tuple:
+def _heads_out(t, name: str, like: torch.Tensor, stream) -> tuple:
     """An output of the shape of `like`, allocated (contiguous) if t is None, and its strides."""
     if t is None:
-        rows, heads, d = like.shape
-        return torch.empty((rows, heads, d), dtype=torch.bfloat16, device=like.device), max(1, heads) * d, d
+        rows, heads, d = shape = like.shape
+        if stream is None and like.is_contiguous():
+            t = torch.empty_like(like)
+        else:
+            t = _empty(like, shape, torch.bfloat16, stream)
+        return t, max(1, heads) * d, d
     strides = _heads(t, name, like.shape[2])
     if t.shape != like.shape:
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
@@ -761,8 +782,8 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
         _need_contig(sin, "sin", torch.float32, (rows, rot // 2))
     if positions is not None:
         _need_contig(positions, "positions", torch.int32, (M,))
-    q_out, ldqo, hsqo = _heads_out(q_out, "q_out", q)
-    k_out, ldko, hsko = _heads_out(k_out, "k_out", k)
+    q_out, ldqo, hsqo = _heads_out(q_out, "q_out", q, stream)
+    k_out, ldko, hsko = _heads_out(k_out, "k_out", k, stream)
     dev = _one_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
     desc = _QK_DESC.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight) or 0,
                          _ptr(k_weight) or 0, _ptr(cos) or 0, _ptr(sin) or 0, _ptr(positions) or 0, M, rows, ldq, hsq,
@@ -800,7 +821,7 @@ def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal
         _need_contig(prefix, "prefix", torch.int32, (docs,))
     if slopes is not None:
         _need_contig(slopes, "slopes", torch.float32, (Hq,))
-    out, ldo, hso = _heads_out(out, "out", q)
+    out, ldo, hso = _heads_out(out, "out", q, stream)
     if lse is not None:
         _need_contig(lse, "lse", torch.float32, (Tq, Hq))
     dev = _one_device(q, k, v, cu_q, cu_k, prefix, slopes, out, lse)
