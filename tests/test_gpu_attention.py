@@ -229,6 +229,37 @@ def test_hidden_keys_may_hold_anything(w8, kernel):
         assert bool(torch.isnan(out[sees]).all()) and bool(torch.isfinite(out[~sees]).all())
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_head_major_everything(w8, kernel):
+    """[heads, tokens, D] tensors: a token stride below the head stride, for every operand."""
+    q, k, v = [tensor(h, n, 64, seed=i).transpose(0, 1) for i, (h, n) in enumerate([(4, 333), (2, 401), (2, 401)])]
+    out = torch.full((6, 333, 64), 3.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(333, 4, device=DEV)
+    w8.w8a8_attention(q, k, v, causal=True, out=out[1:-1].transpose(0, 1), lse=lse, kernel=kernel)
+    check(out[1:-1].transpose(0, 1), lse, q, k, v, [0, 333], [0, 401], 64 ** -0.5, causal=True)
+    assert bool((out[0] == 3).all()) and bool((out[-1] == 3).all())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_queries_in_equal_parts_keys_ragged(w8, kernel):
+    """One of the two streams with starts, the other in equal parts; key and value streams of their own strides."""
+    lk = [5, 200, 0, 131]
+    q, k = tensor(4 * 9, 2, 128), tensor(sum(lk), 2, 128, seed=2)
+    v = tensor(sum(lk), 3, 128, seed=3)[:, :2]
+    lse = torch.empty(36, 2, device=DEV)
+    out = w8.w8a8_attention(q, k, v, cu_k=starts(lk), lse=lse, kernel=kernel)
+    check(out, lse, q, k, v, starts([9] * 4), starts(lk), 128 ** -0.5)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_biases_that_grow_and_vanish(w8, kernel):
+    """Negative, zero and steep slopes, keys on both sides of a query."""
+    slopes = torch.tensor([-0.01, 0.0, 3.0, 0.25], device=DEV)
+    case(w8, [(150, 150), (7, 260), (1, 33)], 4, 2, 64, slopes=slopes, kernel=kernel)
+    prefix = torch.tensor([100, 7, 0], dtype=torch.int32, device=DEV)
+    case(w8, [(150, 150), (7, 260), (1, 33)], 4, 2, 128, slopes=slopes, causal=True, prefix=prefix, kernel=kernel)
+
+
 def test_equal_parts_without_starts(w8):
     q, k, v = tensor(6 * 50, 4, 64), tensor(6 * 70, 2, 64, seed=2), tensor(6 * 70, 2, 64, seed=3)
     got = w8.w8a8_attention(q, k, v, docs=6, causal=True)

@@ -95,7 +95,7 @@ def attention(w8, **change):
     (dict(heads_q=65537), 1), (dict(head_dim=96), 1), (dict(head_dim=256), 1), (dict(cu_q=None, tokens_q=5), 1),
     (dict(cu_k=None, tokens_k=7), 1), (dict(causal=2), 1), (dict(kernel=3), 1), (dict(kernel=-1), 1), (dict(prefix=A), 1), (dict(scale=0.0), 1),
     (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(cap=-1.0), 1),
-    (dict(cap=float("nan")), 1), (dict(cap=2e6), 1), (dict(q=None), 1), (dict(v=None), 1), (dict(out=None), 1),
+    (dict(cap=float("nan")), 1), (dict(cap=2e6), 1), (dict(cap=1e-7), 1), (dict(scale=1e-13), 1), (dict(scale=2e6), 1), (dict(q=None), 1), (dict(v=None), 1), (dict(out=None), 1),
     (dict(ldq=32), 1), (dict(ldk=0), 1), (dict(hsq=0), 1), (dict(ldo=64), 1), (dict(hso=8), 1), (dict(ldv=2 ** 31), 1),
     (dict(ldk=-64), 1), (dict(k=A + 8), 2), (dict(out=A + 2), 2), (dict(ldv=68), 2), (dict(hsq=68, ldq=136), 2),
     (dict(cu_q=A + 2), 2), (dict(lse=A + 1), 2), (dict(slopes=A + 2), 2),

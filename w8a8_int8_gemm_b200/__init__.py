@@ -769,17 +769,20 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     ldk, hsk = _heads(k, "k", D)
     if k.shape[0] != M:
         raise ValueError(f"q has {M} tokens, k has {k.shape[0]}")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need_contig(w, name, torch.bfloat16, (D,))
+    if q_weight is not None:
+        _need_contig(q_weight, "q_weight", torch.bfloat16, (D,))
+    if k_weight is not None:
+        _need_contig(k_weight, "k_weight", torch.bfloat16, (D,))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     rows = rot = 0
     if cos is not None:
-        _need(cos, "cos", torch.float32, 2)
-        rows, rot = cos.shape[0], 2 * cos.shape[1]
-        _need_contig(cos, "cos", torch.float32, (rows, rot // 2))
-        _need_contig(sin, "sin", torch.float32, (rows, rot // 2))
+        if not (isinstance(cos, torch.Tensor) and len(cos.shape) == 2):
+            _need(cos, "cos", torch.float32, 2)
+        table = cos.shape
+        rows, rot = table[0], 2 * table[1]
+        _need_contig(cos, "cos", torch.float32, table)
+        _need_contig(sin, "sin", torch.float32, table)
     if positions is not None:
         _need_contig(positions, "positions", torch.int32, (M,))
     q_out, ldqo, hsqo = _heads_out(q_out, "q_out", q, stream)

@@ -41,7 +41,9 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
   if (a->causal != 0 && a->causal != 1) return W8A8_ERR_INVALID_ARG;
   if (a->kernel < W8A8_ATTENTION_AUTO || a->kernel > W8A8_ATTENTION_TILES) return W8A8_ERR_INVALID_ARG;
   if (a->prefix != nullptr && !a->causal) return W8A8_ERR_INVALID_ARG;
-  if (!(a->scale > 0.0f) || a->scale > 3.0e38f || !(a->cap >= 0.0f) || a->cap > 1.0e6f) return W8A8_ERR_INVALID_ARG;
+  // (scale / cap stays within binary32, and a cap's error within the scores')
+  if (!(a->scale >= 1.0e-12f && a->scale <= 1.0e6f)) return W8A8_ERR_INVALID_ARG;
+  if (!(a->cap == 0.0f || (a->cap >= 1.0e-6f && a->cap <= 1.0e6f))) return W8A8_ERR_INVALID_ARG;
   if (a->tokens_q == 0) return W8A8_OK;
   const View views[4] = {{a->q, a->tokens_q, a->ldq, a->heads_q, a->hsq},
                          {a->k, a->tokens_k, a->ldk, a->heads_k, a->hsk},
