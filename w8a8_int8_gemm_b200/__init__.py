@@ -688,8 +688,8 @@ def _linear_glu(fn, what, code, x, wq, scale_w, bias, out, act, ws_xq, ws_scale_
         _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
         xq_ptr, sa_ptr = ws_xq.data_ptr(), ws_scale_a.data_ptr()
         dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
-    _check(_call(dev, fn, x.data_ptr(), wq.data_ptr(), scale_w.data_ptr(), _ptr(bias), out.data_ptr(), xq_ptr, sa_ptr, M,
-                 N, K, int(act), _stream(stream, dev)), what)
+    _check(_call(dev, fn, x.data_ptr(), wq.data_ptr(), scale_w.data_ptr(), _ptr(bias), out.data_ptr(), xq_ptr, sa_ptr,
+                 M, N, K, int(act), _stream(stream, dev)), what)
     return out
 
 
@@ -746,7 +746,8 @@ def _one_device(*tensors) -> torch.device:
     index = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
-            raise ValueError(f"tensors are on different devices: {sorted({str(t.device) for t in tensors if t is not None})}")
+            devices = sorted({str(t.device) for t in tensors if t is not None})
+            raise ValueError(f"tensors are on different devices: {devices}")
     return tensors[0].device
 
 

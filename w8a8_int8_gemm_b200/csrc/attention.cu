@@ -96,16 +96,17 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
   p.timeout_ns = wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // The kernel that takes less for documents of the average length.  The tile kernel needs about 5 us beside an item's
-  // tiles of 80 keys, which take 0.9 us with up to 128 queries and 1.1 us with more.  (Measured, row kernel against tile
-  // kernel: one document of 2304 keys, 24 heads, 16 queries 13 | 32 us, 64 queries 23 | 32, 128 queries 45 | 33; 16 000
-  // keys, 8 key/value heads of 4: 128 rows 65 | 183, 512 rows 214 | 184.)
+  // tiles of 80 keys, which take 0.9 us with up to 128 queries and 1.1 us with more.  (Measured, row kernel against
+  // tile kernel: one document of 2304 keys, 24 heads, 16 queries 13 | 32 us, 64 queries 23 | 32, 128 queries 45 | 33;
+  // 16 000 keys, 8 key/value heads of 4: 128 rows 65 | 183, 512 rows 214 | 184.)
   int splits;
   const double by_rows = rows_cost(p, sms, &splits);
   const int64_t queries = (a->tokens_q + a->docs - 1) / a->docs;
   const int64_t items = (queries + 255) / 256 * a->docs * a->heads_q;
   const double tiles = static_cast<double>(a->tokens_k / a->docs) / 80.0;
   const double by_tiles = static_cast<double>((items + sms - 1) / sms) * (5.0 + tiles * (queries > 128 ? 1.1 : 0.9));
-  const bool by_row_kernel = a->kernel == W8A8_ATTENTION_AUTO ? by_rows <= by_tiles : a->kernel == W8A8_ATTENTION_ROWS;
+  const bool by_row_kernel =
+      a->kernel == W8A8_ATTENTION_AUTO ? by_rows <= by_tiles : a->kernel == W8A8_ATTENTION_ROWS;
   if (by_row_kernel) return status_of(launch_attention_rows(p, a->head_dim, sms, s));
   return status_of(launch_attention_tiles(p, a->head_dim, s));
 }

@@ -31,8 +31,8 @@ struct AttnParams {
 };
 
 // {64 values, tokens, heads} boxes of 64 x box_rows x 1 of a bf16 [tokens, heads, D] tensor, 128-byte swizzle.
-inline bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld, int64_t hs,
-                  int box_rows) {
+inline bool encode_heads(CUtensorMap* map, const void* base, int D, int64_t tokens, int64_t heads, int64_t ld,
+                         int64_t hs, int box_rows) {
   EncodeTiledFn fn = get_encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(tokens),

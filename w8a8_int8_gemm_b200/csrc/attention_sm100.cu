@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = warp - 17;
       // Matrix descriptors: the high words are constant, the low ones hold the address (in units of 16 bytes).
       const uint64_t desc_q = make_smem_desc_k_sw128(smem_u32(sQ + s * kQ));
-      const uint64_t desc_k = make_smem_desc_k_sw128(smem_u32(ring)), desc_v = make_smem_desc_n_sw128(smem_u32(ring), kBlock);
+      const uint64_t desc_k = make_smem_desc_k_sw128(smem_u32(ring));
+      const uint64_t desc_v = make_smem_desc_n_sw128(smem_u32(ring), kBlock);
       const uint32_t t_s = tmem + s * kSpan, t_o = tmem + kColO + s * D;
       int stage = 0;
       uint32_t phase = 0, q_phase = 0;
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // The value of the thread with the other half of this query's keys.  One barrier is enough with two buffers in
       // turn: a buffer is written again behind the next tile's barrier, where the partner has read it.  (A warp that
-      // aborts arrives once more, and its partner looks at the flag before it comes back, so that none is left waiting.)
+      // aborts arrives once more, and its partner looks at the flag before it comes back: none is left waiting.)
       const auto partner = [&](float x) {
         float* const at = exchange + (turn & 1) * (4 * kSub) + s * kSub + in_sub;
         ++turn;
@@ -562,9 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float base = m == -INFINITY ? 0.0f : m;
         const uint64_t c2 = both(kChange ? 1.0f : c), minus = both(-base);
         uint64_t sums[2] = {both(0.0f), both(0.0f)};
-        // Weights of 2 N keys.  (A part of the exponentials as polynomials on the FMA units, to relieve the special-function
-        // units, made it slower: 438 us against 427 with an eighth of them, 453 with three eighths, at 2 x 4608 tokens, 24
-        // heads of 128.  Two warps per scheduler do not hide the polynomial's latency.)
+        // Weights of 2 N keys.  (A part of the exponentials as polynomials on the FMA units, to relieve the
+        // special-function units, made it slower: 438 us against 427 with an eighth of them, 453 with three eighths,
+        // at 2 x 4608 tokens, 24 heads of 128.  Two warps per scheduler do not hide the polynomial's latency.)
         const auto weights = [&](const uint32_t* v, auto& w) {
           constexpr int N = sizeof(w) / sizeof(w[0]);
 #pragma unroll
@@ -604,8 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = limit > 0;
       const float inv = any ? 1.0f / l : 0.0f;
       const int64_t token = doc.q0 + i;
-      // The warp's 32 rows x D/2 values, 32 columns at a time through shared memory, so that they leave in segments of 64
-      // bytes (16 bytes a thread, each in a row of its own, keep the load/store units busy for 4 000 cycles an item).
+      // The warp's 32 rows x D/2 values, 32 columns at a time through shared memory, so that they leave in segments
+      // of 64 bytes (16 bytes a thread, each in a row of its own, keep the load/store units busy for 4 000 cycles an
+      // item).
       uint8_t* stage = staging + warp * kStagingBytes;
       const int64_t token0 = doc.q0 + row0 + s * kSub + quarter * 32;
       const int valid = my_rows - quarter * 32;
@@ -626,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float a0 = __uint_as_float(o[8 * y + 2 * z]) * inv, a1 = __uint_as_float(o[8 * y + 2 * z + 1]) * inv;
             w[z] = any ? pack_bf16(a0, a1) : 0u;
           }
-          *reinterpret_cast<uint4*>(stage + (4 * lane + (y ^ ((lane >> 1) & 3))) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + (4 * lane + (y ^ ((lane >> 1) & 3))) * 16) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
 #pragma unroll
@@ -681,7 +684,8 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
-  static_assert(smem <= 232448 && kExchange * 4 + (2 * ring_stages(D) + 20) * 8 + 8 <= kHeadBytes - 32, "shared memory");
+  static_assert(smem <= 232448, "shared memory");
+  static_assert(kExchange * 4 + (2 * ring_stages(D) + 20) * 8 + 8 <= kHeadBytes - 32, "barriers before the answers");
   static std::atomic<uint64_t> set{0};
   e = allow_shared_memory(kernel, smem, set);
   if (e != cudaSuccess) return e;

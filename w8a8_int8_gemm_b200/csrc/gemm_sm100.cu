@@ -861,7 +861,8 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   if constexpr (OUT == GemmOut::kBf16Dequant) {
     ok = ok && encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.M, a.N, 32, 64);
   } else if constexpr (kGlu) {
-    ok = ok && encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.M, a.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    ok = ok &&
+         encode_2d(&tm_d, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, a.M, a.N, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   } else {
     ok = ok && encode_2d(&tm_d, EL == GemmElem::kE4M3 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_INT32,
                          4, a.out, a.M, a.N, 32, 32);

@@ -201,7 +201,9 @@ bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 }  // namespace
 
 bool rows_disjoint(int64_t rows, int64_t ld, int64_t heads, int64_t hs, int64_t dim) {
-  if (heads > 1 && rows > 1) return (hs >= dim && ld >= (heads - 1) * hs + dim) || (ld >= dim && hs >= (rows - 1) * ld + dim);
+  if (heads > 1 && rows > 1) {
+    return (hs >= dim && ld >= (heads - 1) * hs + dim) || (ld >= dim && hs >= (rows - 1) * ld + dim);
+  }
   return (heads <= 1 || hs >= dim) && (rows <= 1 || ld >= dim);
 }
 
