@@ -382,3 +382,28 @@ def test_refusals(w8):
     with pytest.raises(w8.W8A8Error) as e:
         w8.w8a8_attention(q, wide[..., :64], k)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("how", ["plain", "causal bias", "prefix cap"])
+def test_more_items_than_sms(w8, how, D):
+    """The tile kernel's CTAs take several items each, one after the other, of long documents that end inside a tile
+    (some of the heads are checked); twice in a row, with the same bits."""
+    lengths, H = [2047, 15, 2223], 24
+    q, k, v = [tensor(sum(lengths), H, D, seed=50 + i) for i in range(3)]
+    cu = starts(lengths)
+    slopes = 2.0 ** -(torch.arange(H, device=DEV) / 3.0)
+    prefix = torch.tensor([700, 15, 1], dtype=torch.int32, device=DEV)
+    args = {"plain": {}, "causal bias": dict(causal=True, slopes=slopes),
+            "prefix cap": dict(causal=True, prefix=prefix, cap=20.0)}[how]
+    got = []
+    for _ in range(2):
+        lse = torch.full((sum(lengths), H), 9.0, device=DEV)
+        got.append((w8.w8a8_attention(q, k, v, cu_q=cu, cu_k=cu, lse=lse, kernel=w8.ATTENTION_TILES, **args), lse))
+    torch.cuda.synchronize()
+    assert w8.w8a8_read_device_error() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    for h in (0, 3, 11, 23):
+        one = slice(h, h + 1)
+        sub = dict(args, slopes=args["slopes"][one]) if "slopes" in args else args
+        check(got[0][0][:, one], got[0][1][:, one], q[:, one], k[:, one], v[:, one], cu, cu, D ** -0.5, **sub)
