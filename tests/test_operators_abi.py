@@ -3,6 +3,7 @@ checked before any device is touched (no GPU needed)."""
 import ctypes
 
 import pytest
+import torch
 
 import __graft_entry__
 
@@ -109,10 +110,20 @@ def test_attention_needs_arguments(w8):
     assert w8.raw_lib().w8a8_attention(None, None) == 1
 
 
-def test_packed_descriptors_have_the_structures_layout(w8):
-    assert w8._QK_DESC.size == ctypes.sizeof(w8.QkDesc)
-    assert w8._ATTENTION_DESC.size == ctypes.sizeof(w8.AttentionDesc)
-    for layout, desc in ((w8._QK_DESC, w8.QkDesc), (w8._ATTENTION_DESC, w8.AttentionDesc)):
-        values = list(range(1, 1 + len(desc._fields_)))
-        d = desc.from_buffer_copy(layout.pack(*values))
-        assert [getattr(d, name) for name, _ in desc._fields_] == values
+def test_binding_refuses_what_are_no_cuda_tensors(w8):
+    """The native part of the binding names the argument (no device is touched)."""
+    x = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    for f in (w8.w8a8_attention, lambda q, k, v: w8.w8a8_qk_norm_rope(q, k)):
+        with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+            f(None, x, x)
+        with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+            f(x, x, x)
+    for f in (w8.w8a8_linear_glu, w8.w8a8_linear_glu_fp8):
+        with pytest.raises(TypeError, match="x must be a torch.Tensor"):
+            f([1.0], x, x)
+        with pytest.raises(ValueError, match="x must be a CUDA tensor"):
+            f(x[0], x[0], x[0])
+
+
+def test_native_part_of_the_binding_matches_torch(w8):
+    assert w8._calls.torch_version == torch.__version__.split("+")[0]

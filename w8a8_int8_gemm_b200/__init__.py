@@ -4,9 +4,10 @@ The functions below have the names of the C entry points in
 ``include/w8a8.h`` and do argument marshalling only: they check that the
 torch tensors have the layout the C ABI expects, allocate outputs the
 caller did not pass (torch is used for device memory and streams), and call
-the library on the current CUDA stream.  Every step of the computation runs
-in the library's CUDA kernels; there is no fallback.  If the shared object
-has not been built, importing this package raises ImportError.
+the library on the current CUDA stream.  (For the calls whose smallest cases
+are bound by the host that is done natively, in csrc/binding.cpp.)  Every step of the computation runs
+in the library's CUDA kernels; there is no fallback.  If the shared objects
+have not been built, importing this package raises ImportError.
 
 Method: "Realizing Native INT8 Compute for Diffusion Transformers on
 Consumer GPUs: A Fused INT8 GEMM Kernel for Ideogram 4.0" (arXiv
@@ -19,7 +20,6 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-import struct
 
 import torch
 
@@ -91,12 +91,6 @@ class QkDesc(ctypes.Structure):
                 + [("eps", ctypes.c_float)])
 
 
-# The descriptors' layouts for struct, which packs one in a quarter of the time that it takes to fill a ctypes
-# structure (a null pointer is 0).
-_QK_DESC = struct.Struct("@9P10q5if0q")
-_ATTENTION_DESC = struct.Struct("@9P10q6i2f0q")
-
-
 class AttentionDesc(ctypes.Structure):
     """w8a8_attention_desc: the arguments of w8a8_attention."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "out", "lse", "cu_q", "cu_k", "prefix", "slopes")]
@@ -161,7 +155,20 @@ def _load() -> ctypes.CDLL:
     return lib
 
 
+def _load_calls():
+    """The native part of the binding: calls whose smallest cases are bound by the host."""
+    again = "build it first (python w8a8_int8_gemm_b200/build.py, or __graft_entry__.build())"
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise ImportError(f"_calls.so is missing or does not load ({e}): {again}") from e
+    if calls.torch_version != torch.__version__.split("+")[0]:
+        raise ImportError(f"_calls.so was built against torch {calls.torch_version}, not {torch.__version__}: {again}")
+    return calls
+
+
 _lib = _load()
+_calls = _load_calls()
 
 
 def exported_names() -> list[str]:
@@ -187,6 +194,13 @@ def _stream(stream, device) -> int | None:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _handle(stream) -> int | None:
+    """A stream for a native call: its handle, or None for the current one of the tensors' device."""
+    if stream is None or isinstance(stream, int):
+        return stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -664,81 +678,29 @@ def w8a8_gemm_glu_fp8(xq, wq, scale_a, scale_w, bias=None, out=None, act: int = 
     return w8a8_gemm_glu_fp8_ex(xq, wq, scale_a, scale_w, bias, out, act, None, stream)
 
 
-def _linear_glu(fn, what, code, x, wq, scale_w, bias, out, act, ws_xq, ws_scale_a, stream):
-    if not (isinstance(x, torch.Tensor) and len(x.shape) == 2):
-        _need(x, "x", torch.bfloat16, 2)
-    M, K = x.shape
-    _need_contig(x, "x", torch.bfloat16, (M, K))
-    N = _glu_weight(wq, code, K, scale_w, bias)
-    if out is None:
-        out = _empty(x, (M, N), torch.bfloat16, stream)
-    else:
-        _need_contig(out, "out", torch.bfloat16, (M, N))
-    if ws_xq is None and ws_scale_a is None:
-        # one allocation for both: the codes, then the scales (16-byte aligned)
-        scales = (M * K + 15) // 16 * 16
-        ws = _empty(x, (scales + 4 * M,), torch.uint8, stream)
-        xq_ptr = ws.data_ptr()
-        sa_ptr = xq_ptr + scales
-        dev = _one_device(x, wq, scale_w, bias, out)
-    else:
-        ws_xq = _empty(x, (M, K), code, stream) if ws_xq is None else ws_xq
-        ws_scale_a = _empty(x, (M,), torch.float32, stream) if ws_scale_a is None else ws_scale_a
-        _need_contig(ws_xq, "ws_xq", code, (M, K))
-        _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
-        xq_ptr, sa_ptr = ws_xq.data_ptr(), ws_scale_a.data_ptr()
-        dev = _one_device(x, wq, scale_w, bias, out, ws_xq, ws_scale_a)
-    _check(_call(dev, fn, x.data_ptr(), wq.data_ptr(), scale_w.data_ptr(), _ptr(bias), out.data_ptr(), xq_ptr, sa_ptr,
-                 M, N, K, int(act), _stream(stream, dev)), what)
-    return out
+def _called(result, what):
+    """What a native call returned: its output, or the status of a refused one."""
+    if result.__class__ is int:
+        raise W8A8Error(result, what)
+    return result
 
 
 def w8a8_linear_glu(x, wq, scale_w, bias=None, out=None, act: int = ACT_SILU, ws_xq=None, ws_scale_a=None,
                     stream=None):
     """The gated linear layer of an MLP: out bf16 [M, N] = act(x Wg^T + bg) * (x Wu^T + bu) from bf16 x [M, K]
     and int8 wq [2N, K] (gate rows, then up rows); workspaces as in w8a8_linear."""
-    return _linear_glu(_lib.w8a8_linear_glu, "w8a8_linear_glu", torch.int8, x, wq, scale_w, bias, out, act, ws_xq,
-                       ws_scale_a, stream)
+    return _called(_calls.linear_glu(x, wq, scale_w, bias, out, act, ws_xq, ws_scale_a, False, _handle(stream)),
+                   "w8a8_linear_glu")
 
 
 def w8a8_linear_glu_fp8(x, wq, scale_w, bias=None, out=None, act: int = ACT_SILU, ws_xq=None, ws_scale_a=None,
                         stream=None):
     """w8a8_linear_glu with E4M3 codes (wq and ws_xq torch.uint8)."""
-    return _linear_glu(_lib.w8a8_linear_glu_fp8, "w8a8_linear_glu_fp8", torch.uint8, x, wq, scale_w, bias, out, act,
-                       ws_xq, ws_scale_a, stream)
+    return _called(_calls.linear_glu(x, wq, scale_w, bias, out, act, ws_xq, ws_scale_a, True, _handle(stream)),
+                   "w8a8_linear_glu_fp8")
 
 
 # ------------------------------------------------- between QKV and attention
-
-
-def _heads(t: torch.Tensor, name: str, dim: int | None = None) -> tuple:
-    """Checks a bf16 [tokens, heads, head_dim] tensor; its (token, head) strides in elements."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.is_cuda and len(t.shape) == 3):
-        _need(t, name, torch.bfloat16, 3)
-    rows, heads, d = t.shape
-    ld, hs, one = t.stride()
-    if one != 1 and t.numel() > 0:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    if dim is not None and d != dim:
-        raise ValueError(f"{name} must have head dimension {dim}, got {d}")
-    if heads <= 1:
-        hs = d
-    return (ld if rows > 1 else max(1, heads) * hs), hs
-
-
-def _heads_out(t, name: str, like: torch.Tensor, stream) -> tuple:
-    """An output of the shape of `like`, allocated (contiguous) if t is None, and its strides."""
-    if t is None:
-        rows, heads, d = shape = like.shape
-        if stream is None and like.is_contiguous():
-            t = torch.empty_like(like)
-        else:
-            t = _empty(like, shape, torch.bfloat16, stream)
-        return t, max(1, heads) * d, d
-    strides = _heads(t, name, like.shape[2])
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    return t, *strides
 
 
 def _one_device(*tensors) -> torch.device:
@@ -765,35 +727,8 @@ def w8a8_qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, po
     values, in one pass -> (q_out, k_out), allocated here (contiguous) if not given; q_out=q, k_out=k works in
     place.  q and k may be strided views, e.g. of one QKV buffer.  cos, sin fp32 [rows, R/2], read at row
     positions[m] (int32 [M]) or m; without them the norm alone."""
-    ldq, hsq = _heads(q, "q")
-    M, hq, D = q.shape
-    ldk, hsk = _heads(k, "k", D)
-    if k.shape[0] != M:
-        raise ValueError(f"q has {M} tokens, k has {k.shape[0]}")
-    if q_weight is not None:
-        _need_contig(q_weight, "q_weight", torch.bfloat16, (D,))
-    if k_weight is not None:
-        _need_contig(k_weight, "k_weight", torch.bfloat16, (D,))
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin come together")
-    rows = rot = 0
-    if cos is not None:
-        if not (isinstance(cos, torch.Tensor) and len(cos.shape) == 2):
-            _need(cos, "cos", torch.float32, 2)
-        table = cos.shape
-        rows, rot = table[0], 2 * table[1]
-        _need_contig(cos, "cos", torch.float32, table)
-        _need_contig(sin, "sin", torch.float32, table)
-    if positions is not None:
-        _need_contig(positions, "positions", torch.int32, (M,))
-    q_out, ldqo, hsqo = _heads_out(q_out, "q_out", q, stream)
-    k_out, ldko, hsko = _heads_out(k_out, "k_out", k, stream)
-    dev = _one_device(q, k, q_weight, k_weight, cos, sin, positions, q_out, k_out)
-    desc = _QK_DESC.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight) or 0,
-                         _ptr(k_weight) or 0, _ptr(cos) or 0, _ptr(sin) or 0, _ptr(positions) or 0, M, rows, ldq, hsq,
-                         ldk, hsk, ldqo, hsqo, ldko, hsko, hq, k.shape[1], D, rot, int(layout), float(eps))
-    _check(_call(dev, _lib.w8a8_qk_norm_rope, desc, _stream(stream, dev)), "w8a8_qk_norm_rope")
-    return q_out, k_out
+    return _called(_calls.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, layout, q_out, k_out,
+                                       _handle(stream)), "w8a8_qk_norm_rope")
 
 
 def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal: bool = False, cu_q=None, cu_k=None,
@@ -807,34 +742,9 @@ def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal
     (int32 [docs]) shows each query the keys up to its own place and the document's prefix; slopes (fp32 [Hq])
     subtracts slope * distance.  lse: fp32 [Tq, Hq] tensor that receives the scores' log-sum-exp.  kernel:
     ATTENTION_ROWS or ATTENTION_TILES by name, for sweeps and tests.  See include/w8a8.h."""
-    ldq, hsq = _heads(q, "q")
-    Tq, Hq, D = q.shape
-    ldk, hsk = _heads(k, "k", D)
-    ldv, hsv = _heads(v, "v", D)
-    Tk, Hk = k.shape[:2]
-    if v.shape != k.shape:
-        raise ValueError(f"v must have the shape of k, got {tuple(v.shape)} and {tuple(k.shape)}")
-    if docs is None:
-        starts = cu_q if cu_q is not None else cu_k
-        docs = 1 if starts is None else starts.shape[0] - 1
-    if cu_q is not None:
-        _need_contig(cu_q, "cu_q", torch.int32, (docs + 1,))
-    if cu_k is not None:
-        _need_contig(cu_k, "cu_k", torch.int32, (docs + 1,))
-    if prefix is not None:
-        _need_contig(prefix, "prefix", torch.int32, (docs,))
-    if slopes is not None:
-        _need_contig(slopes, "slopes", torch.float32, (Hq,))
-    out, ldo, hso = _heads_out(out, "out", q, stream)
-    if lse is not None:
-        _need_contig(lse, "lse", torch.float32, (Tq, Hq))
-    dev = _one_device(q, k, v, cu_q, cu_k, prefix, slopes, out, lse)
-    desc = _ATTENTION_DESC.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(lse) or 0,
-                                _ptr(cu_q) or 0, _ptr(cu_k) or 0, _ptr(prefix) or 0, _ptr(slopes) or 0, Tq, Tk, ldq,
-                                hsq, ldk, hsk, ldv, hsv, ldo, hso, docs, Hq, Hk, D, 1 if causal else 0, kernel,
-                                float(D ** -0.5 if scale is None else scale), float(cap))
-    _check(_call(dev, _lib.w8a8_attention, desc, _stream(stream, dev)), "w8a8_attention")
-    return out
+    return _called(_calls.attention(q, k, v, scale, cap, causal, cu_q, cu_k, docs, prefix, slopes, out, lse, kernel,
+                                    _handle(stream)), "w8a8_attention")
+
 
 
 # ------------------------------------------------- chains of linear layers
