@@ -139,7 +139,8 @@ struct Params {
   // more than half of L2 (long-K layers: A is then streamed once per tile
   // row and would push B out, which every tile row reads again).
   int a_evict_first;
-  int gelu;  // kGlu: the gate's activation (GELU, else SiLU)
+  int gelu;    // kGlu: the gate's activation (GELU, else SiLU)
+  int a_rows;  // kGlu on single CTAs: rows of A's boxes
   // Fused linear layer only: the bf16 activations, the workspace the kernel
   // quantizes them into (xq is also the A operand of tm_a), and the
   // row-block counters ([m_tiles] blocks + 1 CTA counter, zero on entry).
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fills == 0) pdl_wait_prerequisites();  // A may be written by the kernel before this one
             tma_load_2d_pair_hint(sA + stage * kA, &tm_a, bar, kb * kBlockK, a_row, a_pol);
           } else {
-            mbar_arrive_expect_tx(&full[stage], tx_bytes);
+            mbar_arrive_expect_tx(&full[stage], kGlu ? static_cast<uint32_t>(p.a_rows * kBlockK) + kB : tx_bytes);
             if constexpr (kGlu) {
               tma_load_2d_hint(sB + stage * kB, &tm_b_half, &full[stage], kb * kBlockK, b_row, keep);
               tma_load_2d_hint(sB + stage * kB + kB / 2, &tm_b_half, &full[stage], kb * kBlockK, p.N + b_row, keep);
@@ -849,12 +850,16 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   std::memset(&tm_b, 0, sizeof tm_b);
   std::memset(&tm_b_half, 0, sizeof tm_b_half);
   std::memset(&tm_d, 0, sizeof tm_d);
+  // Few tokens: A's boxes hold no more rows than there are (in groups of 8, as the swizzle lays them out).  The MMA
+  // multiplies whatever the tile's other rows hold, in accumulator rows that are not stored; to fill them with zeros
+  // takes the loads as long as that many rows of weights.
+  const int a_rows = kGlu && !PAIR && a.M < kBlockM ? static_cast<int>((a.M + 7) / 8 * 8) : kBlockM;
   bool ok;
   if constexpr (KCH == 2) {
     ok = encode_chunks(&tm_a, a.xq, a.M, a.K, kBlockM) && encode_chunks(&tm_b, a.wq, w_rows, a.K, kBRows) &&
          encode_chunks(&tm_b_half, a.wq, w_rows, a.K, kBRows / 2);
   } else {
-    ok = encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, a.M, a.K, kBlockM, kBlockK) &&
+    ok = encode_2d(&tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.xq, a.M, a.K, a_rows, kBlockK) &&
          encode_2d(&tm_b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, w_rows, a.K, kBRows, kBlockK) &&
          encode_2d(&tm_b_half, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.wq, w_rows, a.K, kBRows / 2, kBlockK);
   }
@@ -887,6 +892,7 @@ cudaError_t launch_typed(const GemmArgs& a, const GemmConfig& cfg, cudaStream_t 
   p.timeout_ns = a.timeout_ns;
   p.err = nullptr;
   p.gelu = a.act == W8A8_ACT_GELU;
+  p.a_rows = a_rows;
   p.a_evict_first = a.M * a.K > a.l2_bytes / 2 ? 1 : 0;
   p.x = static_cast<const __nv_bfloat16*>(a.x);
   p.ldx = a.ldx;
