@@ -323,6 +323,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = (rank == 0);
+  // The one thread that loads or issues.  (Elected, the compiler knows that it is alone.)
+  const auto one = [&] {
+    if constexpr (kGlu) return elect_one();
+    return lane == 0;
+  };
   // Tiles are walked per CTA (single) or per CTA pair.
   const int unit = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);
   const int num_units = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < p.k_blocks; ++kb) {
         ok = warp_wait(&empty[stage], phase ^ 1u, abort_flag, p.timeout_ns, p.err, kSiteProducerEmpty);
         if (!ok) break;
-        if (lane == 0) {
+        if (one()) {
           if constexpr (PAIR && KCH == 2) {
             // 3-D maps {128 B, rows, K-chunk}: one box = this CTA's rows x two chunks
             const uint32_t bar = map_to_cta(smem_u32(&full[stage]), 0u);
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = warp_wait(&full[stage], phase, abort_flag, p.timeout_ns, p.err, kSiteMmaFull);
           if (!ok) break;
           tc_fence_after_sync();
-          if (lane == 0) {
+          if (one()) {
 #pragma unroll
             for (int kk = 0; kk < KCH * (kBlockK / kMmaK); ++kk) {
               // Chunk c of the stage, then K=32 slice k inside its 128-byte
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (one()) {
           if constexpr (PAIR) {
             mma_commit_pair(smem_u32(&tfull[buf]));
             mma_commit_pair(map_to_cta(smem_u32(&tfull[buf]), 1u));
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok && PAIR && lane == 0) st_cluster_u32(peer_abort, 1u);
       // Teardown: no MMA may still write tensor memory when it is freed.
-      if (lane == 0) {
+      if (one()) {
         if constexpr (PAIR) {
           mma_commit_pair(smem_u32(drain));
         } else {
