@@ -5,9 +5,10 @@ The functions below have the names of the C entry points in
 torch tensors have the layout the C ABI expects, allocate outputs the
 caller did not pass (torch is used for device memory and streams), and call
 the library on the current CUDA stream.  (For the calls whose smallest cases
-are bound by the host that is done natively, in csrc/binding.cpp.)  Every step of the computation runs
-in the library's CUDA kernels; there is no fallback.  If the shared objects
-have not been built, importing this package raises ImportError.
+are bound by the host that is done natively, in csrc/binding.cpp.)  Every
+step of the computation runs in the library's CUDA kernels; there is no
+fallback.  If the shared objects have not been built, importing this package
+raises ImportError.
 
 Method: "Realizing Native INT8 Compute for Diffusion Transformers on
 Consumer GPUs: A Fused INT8 GEMM Kernel for Ideogram 4.0" (arXiv

@@ -52,6 +52,10 @@
 // one of them anyway).  The MMAs bound it, as they bound the plain layer: the
 // gate's exponential and division, two special-function operations per
 // output, run in the epilogue warps beside the next tile's MMAs.
+// Measured, quantizer included, in a graph of calls: 4096 tokens, N 8192, K
+// 3072, SiLU, int8 141 us (2.92 POP/s, 0.87 of twice the measured bf16 rate);
+// 2305 tokens, N 5640, K 2048, GELU, E4M3 51 us (2.11 PFLOP/s; a last round of
+// half-empty SMs); one token, N 8192, K 2048 10.4 us (3.2 TB/s of weights).
 //
 // Every mbarrier wait is bounded in time (see sm100_ptx.cuh); on timeout the
 // kernel records the site in the device error word, lets its in-flight
@@ -323,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
   const bool leader = (rank == 0);
-  // The one thread that loads or issues.  (Elected, the compiler knows that it is alone.)
+  // The one thread that loads or issues.  Elected, the compiler knows that it is alone, and a K-block takes fewer
+  // instructions (one token, N 8192, K 2048: 11.1 -> 9.8 us).
   const auto one = [&] {
     if constexpr (kGlu) return elect_one();
     return lane == 0;
