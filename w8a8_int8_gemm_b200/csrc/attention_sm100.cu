@@ -41,6 +41,11 @@
 // 128 operations (2048 cycles at D = 128; Q K^T reads its operands at the
 // limit of shared memory and takes 1.2 times its share), and the softmax:
 // 2048 cycles of the special-function units for the exponentials alone.
+// Measured, in graphs of calls: 2 x 4608 tokens, 24 heads of 128: 412 us, 1.27
+// PFLOP/s, 0.76 of the measured bf16 rate (484 us in a loop of seconds, where
+// the board's power cap sets the clock); 2 x 4095 tokens, 16 heads of 128,
+// causal, with slopes: 161 us; 9 ragged prompts of 911 tokens on average, cap
+// and prefix, 16 heads of 64 over 4: 68 us.
 #include <cuda.h>
 
 #include <cstring>

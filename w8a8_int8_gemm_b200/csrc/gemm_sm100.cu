@@ -53,9 +53,9 @@
 // gate's exponential and division, two special-function operations per
 // output, run in the epilogue warps beside the next tile's MMAs.
 // Measured, quantizer included, in a graph of calls: 4096 tokens, N 8192, K
-// 3072, SiLU, int8 141 us (2.92 POP/s, 0.87 of twice the measured bf16 rate);
-// 2305 tokens, N 5640, K 2048, GELU, E4M3 51 us (2.11 PFLOP/s; a last round of
-// half-empty SMs); one token, N 8192, K 2048 10.4 us (3.2 TB/s of weights).
+// 3072, SiLU, int8 136 us (3.04 POP/s, 0.91 of twice the measured bf16 rate);
+// 2305 tokens, N 5640, K 2048, GELU, E4M3 50 us (2.14 PFLOP/s; a last round of
+// half-empty SMs); one token, N 8192, K 2048 10.1 us (3.3 TB/s of weights).
 //
 // Every mbarrier wait is bounded in time (see sm100_ptx.cuh); on timeout the
 // kernel records the site in the device error word, lets its in-flight

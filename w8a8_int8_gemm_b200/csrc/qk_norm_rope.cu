@@ -19,7 +19,7 @@
 // token's table row and the weights once for them.  The arithmetic is on
 // pairs of binary32: one value at a time, with q and k mixed in a warp, the
 // instructions alone took as long as the memory (51 us for 9216 tokens of 48
-// heads of 128; now 43.9 us in a graph of calls, 5.27 TB/s, 0.80 of the
+// heads of 128; now 43.4 us in a graph of calls, 5.3 TB/s, 0.81 of the
 // measured copy rate).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
