@@ -113,3 +113,35 @@ def test_block(w8, Hq, Hk, D, F, lengths, causal):
         b.run(x)
         torch.cuda.synchronize()
         assert torch.equal(b.y, got)
+
+
+def test_two_threads_with_streams_of_their_own(w8):
+    """Calls from two threads at once, each on a stream by handle or object and with outputs and workspaces of the
+    call's own, give the bits of calls one after the other."""
+    import threading
+    q, k = attention_test.tensor(300, 4, 64, seed=1), attention_test.tensor(300, 2, 64, seed=2)
+    x = attention_test.tensor(70, 256, seed=3)
+    wq, sw = w8.w8a8_quantize_weight(torch.randn((2 * 128, 256), device=DEV))
+
+    def calls(stream):
+        return [w8.w8a8_attention(q, k, k, causal=True, stream=stream), *w8.w8a8_qk_norm_rope(q, k, stream=stream),
+                w8.w8a8_linear_glu(x, wq, sw, stream=stream)]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    got, streams = {}, [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def work(i):
+        stream = streams[i] if i else streams[i].cuda_stream
+        got[i] = [calls(stream) for _ in range(50)]
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert w8.w8a8_read_device_error() == 0
+    for i in range(2):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
