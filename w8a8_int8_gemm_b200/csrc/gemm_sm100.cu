@@ -571,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t stream_out = l2_policy_evict_first();  // the output is not read again here
     if constexpr (!FUSE) pdl_wait_prerequisites();  // scale_a may come from the kernel before this one
     int local = 0;
+    int stores = 0;  // kGlu: this warp's, so far
     bool ok = true;
     if constexpr (FUSE) {
       // Per-token quantization of the activations.  Warp w of the grid's
@@ -672,8 +673,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row0 < p.M && col0 < p.N) {
             uint32_t pk[16];
             glu_32<kE4M3>(vg, vu, sa, ps_w + cl, ps_w + out_n + cl, ps_b + cl, ps_b + out_n + cl, p.gelu != 0, pk);
-            // Two staging blocks of 32 rows x 64 bytes in turn (64-byte swizzle).
-            uint8_t* block = sbuf + (sc & 1) * (kEpiBufBytes / 2);
+            // Two staging blocks of 32 rows x 64 bytes (64-byte swizzle), in turn over the warp's stores: the one
+            // before this may still read the other block.  (Not by sc: where the output ends inside a tile, or a
+            // tile has one step, two stores of sc = 0 follow each other.)
+            uint8_t* block = sbuf + (stores & 1) * (kEpiBufBytes / 2);
+            ++stores;
             if (lane == 0) bulk_wait_group_read<1>();
             __syncwarp();
 #pragma unroll
