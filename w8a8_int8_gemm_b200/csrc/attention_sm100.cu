@@ -133,10 +133,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_free = s_full + 2;        // [2] scores read
   uint64_t* p_full = s_free + 2;        // [2] weights ready
   uint64_t* o_full = p_full + 2;        // [2] product with V done: O complete so far, P free
-  // [2] a last V tile that ends inside has landed: two in turn, because the loader may be an item ahead of warp 19
-  // (not two: an item's Q waits for the last item's scores, and those for the product before them).
+  // [2] a last V tile that ends inside has landed, and warp 19 has filled it: two in turn, so that the loader may be an
+  // item ahead of warp 19.  (Without the second wait it could be two ahead, and complete a phase that warp 19 has not
+  // seen: an item's Q waits for the last scores of its own sub-tile alone, and items without sub-tile 0, whose first
+  // queries see no key, do not wait for those without sub-tile 1.)
   uint64_t* tail_full = o_full + 2;
-  uint64_t* drain = tail_full + 2;      // [2]
+  uint64_t* tail_free = tail_full + 2;
+  uint64_t* drain = tail_free + 2;      // [2]
   uint64_t* item_full = drain + 2;      // [2] the next item is known
   uint64_t* item_free = item_full + 2;  // [2] ... and read by every warp
   uint8_t* answer = smem + kHeadBytes - 32;  // [2][16]
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tail_full[s], 1);
+      mbar_init(&tail_free[s], 1);
       mbar_init(&drain[s], 1);
       mbar_init(&item_full[s], 1);
       mbar_init(&item_free[s], kThreads / 32);
@@ -280,7 +284,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; ok && j < it.tiles; ++j) {
             if (j + 1 < it.tiles) load(&tm_k, j + 1, nullptr);
             // (a last V tile that ends inside goes to warp 19 first, which fills the slot)
-            load(&tm_v, j, it.tail && j + 1 == it.tiles ? &tail_full[tails & 1] : nullptr);
+            const bool tail = it.tail && j + 1 == it.tiles;
+            const int t = tails & 1;
+            if (tail && tails >= 2) {
+              ok = ok && wait(&tail_free[t], static_cast<uint32_t>((tails - 2) >> 1) & 1u, kSiteAttnLoad);
+            }
+            load(&tm_v, j, tail ? &tail_full[t] : nullptr);
           }
           tails += it.tail;
           // The item after this one, asked for with the last loads of this one (earlier, and items are dealt out before
@@ -379,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&tail_full[tails & 1], static_cast<uint32_t>(tails >> 1) & 1u, abort_flag, p.timeout_ns, err,
                        kSiteAttnOperand);
         if (!ok) continue;
-        ++tails;
         const int stage = (fills + kStages - 1) % kStages;
         uint8_t* v = ring + stage * kTile;
         for (int e = it.tail_rows * 8 + lane; e < kTileK * 8; e += 32) {
@@ -388,7 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[stage]);
+        if (lane == 0) {
+          mbar_arrive(&full[stage]);
+          mbar_arrive(&tail_free[tails & 1]);
+        }
+        ++tails;
       }
     }
     __syncwarp();
@@ -690,7 +702,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t stream) {
   auto kernel = attention_tiles_kernel<D, CAP, BIAS>;
   constexpr int smem = smem_bytes(D);
   static_assert(smem <= 232448, "shared memory");
-  static_assert(kExchange * 4 + (2 * ring_stages(D) + 20) * 8 + 8 <= kHeadBytes - 32, "barriers before the answers");
+  static_assert(kExchange * 4 + (2 * ring_stages(D) + 22) * 8 + 8 <= kHeadBytes - 32, "barriers before the answers");
   static std::atomic<uint64_t> set{0};
   e = allow_shared_memory(kernel, smem, set);
   if (e != cudaSuccess) return e;
