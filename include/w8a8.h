@@ -463,7 +463,7 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  * head_dim 64 or 128; heads_q a multiple of heads_k, up to 65536; docs >= 1;
  * tokens up to 2^30, and the work items, (tokens_q / 256 + docs) * heads_q,
  * below 2^31; 1e-12 <= scale <= 1e6; cap 0 (none) or 1e-6 .. 1e6 (a cap adds
- * an error of 1e-6 * cap to a score).  tokens_q == 0 launches nothing.
+ * a relative error of 1e-6 to a score).  tokens_q == 0 launches nothing.
  */
 /* Two kernels compute it, for any shape: one reads K and V once for 16 (query,
  * head) rows and splits the keys (single tokens, short documents), one takes

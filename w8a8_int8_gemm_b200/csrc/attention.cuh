@@ -137,10 +137,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// cap * log2(e) * tanh(s * scale / cap), from tanh(y) = 1 - 2 / (1 + exp(2y)):
-// within 3e-7 of tanh, so within 5e-7 * cap of the score.
-__device__ __forceinline__ float capped(float s, float two_log2e_scale_over_cap, float cap_log2e) {
-  return cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(s * two_log2e_scale_over_cap));
+// tanh(y) = y * sum_n k[n] y^2n, least squares on Chebyshev nodes: relative error 7e-7 (evaluated in binary32) for
+// |y| <= 1.
+__device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
+                                       -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
+
+// cap * log2(e) * tanh(y), y = s * scale / cap, to a relative 1e-6.  Within the cap (|y| <= 1) by the polynomial;
+// beyond it as 1 - 2 / (1 + exp(2y)), which is off by 5e-7 of the cap: there no more than that of the score, but for
+// scores far inside a large cap it would be all that is left of them.
+__device__ __forceinline__ float capped(float y, float cap_log2e) {
+  const float u = y * y;
+  float t = kTanh[5];
+#pragma unroll
+  for (int n = 4; n >= 0; --n) t = fmaf(t, u, kTanh[n]);
+  const float beyond = cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(y * (2.0f * kLog2e)));
+  return fabsf(y) <= 1.0f ? t * y * cap_log2e : beyond;
 }
 
 #endif  // __CUDACC__

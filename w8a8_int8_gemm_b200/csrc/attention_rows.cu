@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     const float c_scale = p.scale * kLog2e;
-    const float c_tanh = CAP ? 2.0f * kLog2e * p.scale / p.cap : 0.0f;
+    const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
     const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
     // ldmatrix addresses: block b's row i is lane 8 b + i's.  K: blocks are keys 0-7 | 8-15 x values 0-7 | 8-15 of a
     // step of 16 values (row = key).  V, transposed: keys 0-7 | 8-15 x values 0-7 | 8-15.
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int x = 0; x < 4; ++x) {
           const int h = x >> 1;
           const int j = key0 + 8 * a + 2 * t + (x & 1);
-          float y = CAP ? capped(s[a][x], c_tanh, c_cap) : s[a][x] * c_scale;
+          float y = CAP ? capped(s[a][x] * inv_cap, c_cap) : s[a][x] * c_scale;
           if (BIAS) y -= slope[h] * fabsf(static_cast<float>(place[h] - j));
           s[a][x] = j < limit[h] ? y : -INFINITY;
           top[h] = fmaxf(top[h], s[a][x]);

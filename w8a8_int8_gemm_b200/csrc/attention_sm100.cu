@@ -80,10 +80,7 @@ __host__ __device__ constexpr int smem_bytes(int D) {
   return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D) + kSoftmaxWarps * kStagingBytes;
 }
 
-// tanh(y) = y * sum_n k[n] y^2n, least squares on Chebyshev nodes: relative error 7e-7 (evaluated in binary32) for
-// |y| <= 1 with kTanh and |y| <= 1/4 with kTanhNear.
-__device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
-                                       -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
+// The same as kTanh, for |y| <= 1/4.
 __device__ constexpr float kTanhNear[3] = {9.9999960187e-1f, -3.3321876803e-1f, 1.2841111966e-1f};
 
 // Maximum of three; NaN if one is.
@@ -418,12 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int in_sub = quarter * 32 + lane;
     constexpr bool kChange = CAP || BIAS;  // scores need more than the factor c
     const float c = p.scale * kLog2e;
-    const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
-    const float c_tanh = 2.0f * kLog2e * inv_cap;
+    // The polynomials' coefficients hold the cap times up to the eleventh power of scale / cap, which has to stay
+    // within binary32: where it does not, that factor is applied to the scores first and is 1 in the coefficients.
     const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
-    // A quarter of the cap, as a product of q and k.  (The polynomial's coefficients hold up to the tenth power of
-    // scale / cap, which has to stay within binary32; a NaN among the scores compares false with either bound.)
-    const float near = inv_cap <= 1.0f && inv_cap >= 0x1p-12f ? 0.25f / inv_cap : -1.0f;
+    const float to_cap = CAP ? p.scale / p.cap : 0.0f;
+    const float power4 = to_cap * to_cap * to_cap * to_cap;
+    const bool in_range = to_cap <= 1.0f && c_cap * power4 * power4 * (to_cap * to_cap * to_cap) >= 0x1p-126f;
+    const float inv_cap = in_range ? to_cap : 1.0f;
+    // A quarter of the cap, as a product of q and k.  (A NaN among the scores compares false with either bound.)
+    const float near = 0.25f / inv_cap;
     bool ok = true;
     uint32_t s_phase = 0, o_phase = 0;  // of s_full and o_full
     int turn = 0;                       // of the exchange buffers
@@ -448,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (CAP) {
           // Scores within the cap on either side (all of them, unless the scores are far beyond it) take a polynomial
           // for tanh, in s^2 with the scale and the cap in its coefficients: 4 operations per score within a quarter of
-          // the cap, 7 within the cap.  Others take two special functions each.
+          // the cap, 7 within the cap.  Where there are others, each takes the form that fits it.
+          if (!in_range) {
+#pragma unroll
+            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * to_cap);
+          }
           float far = 0.0f;
 #pragma unroll
           for (int x = 0; x < N; x += 2) {
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             polynomial(std::integral_constant<int, 6>{}, kTanh);
           } else {
 #pragma unroll
-            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]), c_tanh, c_cap));
+            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]) * inv_cap, c_cap));
           }
         }
         if constexpr (BIAS) {
