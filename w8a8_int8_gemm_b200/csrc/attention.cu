@@ -93,6 +93,15 @@ extern "C" w8a8_status w8a8_attention(const w8a8_attention_desc* a, w8a8_stream_
   p.causal = a->causal != 0;
   p.scale = a->scale;
   p.cap = a->cap;
+  p.cap_log2e = p.inv_cap = p.near = p.near_k[0] = p.near_k[1] = p.near_k[2] = 0.0f;
+  if (a->cap > 0.0f) {
+    p.cap_log2e = a->cap * kLog2e;
+    p.inv_cap = a->scale / a->cap;
+    const float square = p.inv_cap * p.inv_cap;
+    float f = p.cap_log2e * p.inv_cap;
+    p.near = p.inv_cap <= 1.0f && f * square * square >= 0x1p-120f ? 0.25f / p.inv_cap : -1.0f;
+    for (int i = 0; i < 3; ++i, f *= square) p.near_k[i] = kTanhNear[i] * f;
+  }
   p.timeout_ns = wait_timeout_ns();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // The kernel that takes less for documents of the average length.  The tile kernel needs about 5 us beside an item's

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "sm100_ptx.cuh"
 
 namespace w8a8 {
 
@@ -27,6 +28,11 @@ struct AttnParams {
   int heads_q, heads_k, group;  // group = heads_q / heads_k
   bool causal;
   float scale, cap;
+  // With a cap, computed on the host to spare the kernels' registers: the cap in units of log2, the factor from a product
+  // of q and k to a score in units of the cap, a quarter of the cap as such a product, and kTanhNear as a polynomial in
+  // the product with the cap's factor in it.  (-1 where its coefficients, the cap times up to the fifth power of the
+  // factor, leave binary32.)
+  float cap_log2e, inv_cap, near, near_k[3];
   uint64_t timeout_ns;
 };
 
@@ -54,7 +60,14 @@ cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, cudaStream
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// tanh(y) = y * sum_n k[n] y^2n, least squares on Chebyshev nodes: relative error 7e-7 (evaluated in binary32) for
+// |y| <= 1 with kTanh (device code) and |y| <= 1/4 with kTanhNear (from which the host makes AttnParams::near_k).
+constexpr float kTanhNear[3] = {9.9999960187e-1f, -3.3321876803e-1f, 1.2841111966e-1f};
+
 #ifdef __CUDACC__
+
+__device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
+                                       -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
 
 // One document: its tokens in the packed streams and its masks.
 struct Doc {
@@ -137,21 +150,37 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh(y) = y * sum_n k[n] y^2n, least squares on Chebyshev nodes: relative error 7e-7 (evaluated in binary32) for
-// |y| <= 1.
-__device__ constexpr float kTanh[6] = {9.9999936384e-1f, -3.3328806676e-1f, 1.3279611505e-1f,
-                                       -5.1555843877e-2f, 1.6687155235e-2f, -3.0449762314e-3f};
-
-// cap * log2(e) * tanh(y), y = s * scale / cap, to a relative 1e-6.  Within the cap (|y| <= 1) by the polynomial;
-// beyond it as 1 - 2 / (1 + exp(2y)), which is off by 5e-7 of the cap: there no more than that of the score, but for
-// scores far inside a large cap it would be all that is left of them.
-__device__ __forceinline__ float capped(float y, float cap_log2e) {
-  const float u = y * y;
-  float t = kTanh[5];
+// cap * log2(e) * tanh(y), y = s * scale / cap, to a relative 1e-6: within the cap (|y| <= 1, two scores at a time) by
+// the polynomial, beyond it as 1 - 2 / (1 + exp(2y)).  (That is off by 5e-7 of the cap: beyond the cap no more than
+// that of the score, but all that is left of a score far inside a large cap.)
+__device__ __forceinline__ uint64_t capped_within(uint64_t y, float cap_log2e) {
+  const uint64_t u = mul2(y, y);
+  uint64_t t = both(kTanh[5]);
 #pragma unroll
-  for (int n = 4; n >= 0; --n) t = fmaf(t, u, kTanh[n]);
-  const float beyond = cap_log2e - __fdividef(2.0f * cap_log2e, 1.0f + ex2(y * (2.0f * kLog2e)));
-  return fabsf(y) <= 1.0f ? t * y * cap_log2e : beyond;
+  for (int n = 4; n >= 0; --n) t = fma2(t, u, both(kTanh[n]));
+  return mul2(mul2(t, y), both(cap_log2e));
+}
+
+__device__ __forceinline__ float capped_beyond(float y, float cap_log2e) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + ex2(y * (2.0f * kLog2e))));
+  return fmaf(-2.0f * cap_log2e, r, cap_log2e);
+}
+
+// Both, for N scores in units of the cap; `beyond` where one of them may lie beyond it.
+template <int N>
+__device__ __forceinline__ void capped(float (&y)[N], bool beyond, float cap_log2e) {
+  float s[N];
+#pragma unroll
+  for (int x = 0; x < N; x += 2) unpair(capped_within(pair(y[x], y[x + 1]), cap_log2e), s[x], s[x + 1]);
+  if (beyond) {
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      if (!(fabsf(y[x]) <= 1.0f)) s[x] = capped_beyond(y[x], cap_log2e);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < N; ++x) y[x] = s[x];
 }
 
 #endif  // __CUDACC__

@@ -180,8 +180,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     const float c_scale = p.scale * kLog2e;
-    const float inv_cap = CAP ? p.scale / p.cap : 0.0f;
-    const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
     // ldmatrix addresses: block b's row i is lane 8 b + i's.  K: blocks are keys 0-7 | 8-15 x values 0-7 | 8-15 of a
     // step of 16 values (row = key).  V, transposed: keys 0-7 | 8-15 x values 0-7 | 8-15.
     const uint32_t k_row = 16 * warp + (lane & 7) + ((lane >> 4) << 3), k_chunk = (lane >> 3) & 1;
@@ -205,6 +203,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         mma_bf16(s[1], qf[x][0], qf[x][1], qf[x][2], qf[x][3], b[2], b[3]);
       }
 
+      if constexpr (CAP) {
+        float far = 0.0f;
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) far = fmaxf(far, fabsf(s[a][x] *= p.inv_cap));
+        }
+        float y[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+        capped(y, far > 1.0f, p.cap_log2e);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) s[x / 4][x % 4] = y[x];
+        __syncwarp();
+      }
       // Scores in units of log2, masked by the rows' limits; s[a][2h + e]: row h, key 8a + 2t + e.
       float top[2] = {m[0], m[1]};
 #pragma unroll
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int x = 0; x < 4; ++x) {
           const int h = x >> 1;
           const int j = key0 + 8 * a + 2 * t + (x & 1);
-          float y = CAP ? capped(s[a][x] * inv_cap, c_cap) : s[a][x] * c_scale;
+          float y = CAP ? s[a][x] : s[a][x] * c_scale;
           if (BIAS) y -= slope[h] * fabsf(static_cast<float>(place[h] - j));
           s[a][x] = j < limit[h] ? y : -INFINITY;
           top[h] = fmaxf(top[h], s[a][x]);

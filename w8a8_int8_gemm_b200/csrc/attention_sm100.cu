@@ -49,7 +49,6 @@
 #include <cuda.h>
 
 #include <cstring>
-#include <type_traits>
 
 #include "attention.cuh"
 #include "internal.h"
@@ -79,9 +78,6 @@ constexpr int kStagingBytes = 2048;  // of a softmax warp's output
 __host__ __device__ constexpr int smem_bytes(int D) {
   return kHeadBytes + 2 * q_bytes(D) + ring_stages(D) * tile_bytes(D) + kSoftmaxWarps * kStagingBytes;
 }
-
-// The same as kTanh, for |y| <= 1/4.
-__device__ constexpr float kTanhNear[3] = {9.9999960187e-1f, -3.3321876803e-1f, 1.2841111966e-1f};
 
 // Maximum of three; NaN if one is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -415,15 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int in_sub = quarter * 32 + lane;
     constexpr bool kChange = CAP || BIAS;  // scores need more than the factor c
     const float c = p.scale * kLog2e;
-    // The polynomials' coefficients hold the cap times up to the eleventh power of scale / cap, which has to stay
-    // within binary32: where it does not, that factor is applied to the scores first and is 1 in the coefficients.
-    const float c_cap = CAP ? p.cap * kLog2e : 0.0f;
-    const float to_cap = CAP ? p.scale / p.cap : 0.0f;
-    const float power4 = to_cap * to_cap * to_cap * to_cap;
-    const bool in_range = to_cap <= 1.0f && c_cap * power4 * power4 * (to_cap * to_cap * to_cap) >= 0x1p-126f;
-    const float inv_cap = in_range ? to_cap : 1.0f;
-    // A quarter of the cap, as a product of q and k.  (A NaN among the scores compares false with either bound.)
-    const float near = 0.25f / inv_cap;
     bool ok = true;
     uint32_t s_phase = 0, o_phase = 0;  // of s_full and o_full
     int turn = 0;                       // of the exchange buffers
@@ -442,50 +429,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int place = i + doc.shift;
       const int first_place = row0 + s * kSub + doc.shift;  // of the sub-tile's queries
 
-      // Scores of a tile, from key key0 of the document on: cap, bias and mask; their maximum.
-      const auto first_pass = [&](auto& v, int key0, bool masked) {
-        constexpr int N = sizeof(v) / sizeof(v[0]);
-        if constexpr (CAP) {
-          // Scores within the cap on either side (all of them, unless the scores are far beyond it) take a polynomial
-          // for tanh, in s^2 with the scale and the cap in its coefficients: 4 operations per score within a quarter of
-          // the cap, 7 within the cap.  Where there are others, each takes the form that fits it.
-          if (!in_range) {
-#pragma unroll
-            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * to_cap);
-          }
-          float far = 0.0f;
+      // The cap, on a thread's scores of a tile, from key key0 of the document on.  Scores within the cap on either side
+      // (all of them, unless the scores are far beyond it) take a polynomial for tanh: 4 operations for two scores within
+      // a quarter of the cap, in s^2 with the scale and the cap in its coefficients; 8 within the cap.  Where there are
+      // others, each score takes the form that fits it.  The choice is the thread's, over the keys that its query sees:
+      // other queries, hidden keys and other documents must not change a query's bits.
+      const auto cap_pass = [&](auto& va, auto& vb, int key0, bool masked) {
+        const auto farthest = [](const auto& v, float far) {
+          constexpr int N = sizeof(v) / sizeof(v[0]);
 #pragma unroll
           for (int x = 0; x < N; x += 2) {
             far = max3(far, fabsf(__uint_as_float(v[x])), fabsf(__uint_as_float(v[x + 1])));
           }
-          const auto polynomial = [&](auto terms, const float* k) {
-            constexpr int T = decltype(terms)::value;
-            uint64_t a[T];
-            float f = c_cap * inv_cap;
+          return far;
+        };
+        const auto hide = [](auto& v, int left) {
+          constexpr int N = sizeof(v) / sizeof(v[0]);
 #pragma unroll
-            for (int y = 0; y < T; ++y, f *= inv_cap * inv_cap) a[y] = both(k[y] * f);
+          for (int x = 0; x < N; ++x) {
+            if (x >= left) v[x] = 0u;
+          }
+        };
+        float far = farthest(vb, farthest(va, 0.0f));
+        if (masked && !__all_sync(0xFFFFFFFFu, far <= p.near)) {
+          hide(va, limit - key0);
+          hide(vb, limit - key0 - 32);
+          far = farthest(vb, farthest(va, 0.0f));
+        }
+        if (far <= p.near) {  // (a NaN among the scores compares false)
+          const uint64_t k0 = both(p.near_k[0]), k1 = both(p.near_k[1]), k2 = both(p.near_k[2]);
+          const auto nearby = [&](auto& v) {
+            constexpr int N = sizeof(v) / sizeof(v[0]);
 #pragma unroll
             for (int x = 0; x < N; x += 2) {
-              const uint64_t y = pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
-              const uint64_t u = mul2(y, y);
-              uint64_t t = a[T - 1];
-#pragma unroll
-              for (int z = T - 2; z >= 0; --z) t = fma2(t, u, a[z]);
+              const uint64_t y = pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), u = mul2(y, y);
               float a0, a1;
-              unpair(mul2(t, y), a0, a1);
+              unpair(mul2(fma2(fma2(k2, u, k1), u, k0), y), a0, a1);
               v[x] = __float_as_uint(a0);
               v[x + 1] = __float_as_uint(a1);
             }
           };
-          if (__all_sync(0xFFFFFFFFu, far <= near)) {
-            polynomial(std::integral_constant<int, 3>{}, kTanhNear);
-          } else if (__all_sync(0xFFFFFFFFu, far <= 4.0f * near)) {
-            polynomial(std::integral_constant<int, 6>{}, kTanh);
-          } else {
+          nearby(va);
+          nearby(vb);
+        } else {
+          // (one stretch of code within and beyond the cap, a few scores at a time: with one for each, 604 us against
+          // 534 for 4608 tokens, 24 heads of 128 and a cap of 3, three times the scores' deviation)
+          const bool beyond = !(far * p.inv_cap <= 1.0f);
+          const auto rest = [&](auto& v) {
+            constexpr int N = sizeof(v) / sizeof(v[0]);
 #pragma unroll
-            for (int x = 0; x < N; ++x) v[x] = __float_as_uint(capped(__uint_as_float(v[x]) * inv_cap, c_cap));
-          }
+            for (int at = 0; at < N; at += 8) {
+              float y[8];
+#pragma unroll
+              for (int x = 0; x < 8; x += 2) {
+                const uint64_t two = pair(__uint_as_float(v[at + x]), __uint_as_float(v[at + x + 1]));
+                unpair(mul2(two, both(p.inv_cap)), y[x], y[x + 1]);
+              }
+              capped(y, beyond, p.cap_log2e);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) v[at + x] = __float_as_uint(y[x]);
+            }
+          };
+          rest(va);
+          rest(vb);
         }
+        __syncwarp();
+      };
+
+      // Scores of a tile, from key key0 of the document on: bias and mask; their maximum.
+      const auto first_pass = [&](auto& v, int key0, bool masked) {
+        constexpr int N = sizeof(v) / sizeof(v[0]);
         if constexpr (BIAS) {
           const float f = CAP ? 1.0f : c;
           const float first = static_cast<float>(key0 - place);  // distance of the first key, signed
@@ -551,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[s]);
+        if constexpr (CAP) cap_pass(va, vb, key0, masked);
         float top = fmax_nan(first_pass(va, key0, masked), first_pass(vb, key0 + 32, masked));
         top = fmax_nan(top, partner(top));
         if (!kChange) top *= c;  // c > 0
