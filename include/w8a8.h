@@ -437,8 +437,8 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  *   out[i,h,:] = sum_j softmax_j(s)[j] * v[j,h',:]  over the keys seen
  *   lse[i,h] = log sum_j exp(s[j])                  over the keys seen
  * (the last query stands at the last key, as in a cache; a prefix longer than
- * the document is the whole document).  A query that sees no key gets 0 and an
- * lse of -inf.  Scores, maxima, sums and weighted sums are binary32; the
+ * the document is the whole document).  A query that sees no key, or only keys
+ * whose scores are -inf, gets 0 and an lse of -inf.  Scores, maxima, sums and weighted sums are binary32; the
  * weights exp(s - max) enter the product with v in bf16 (in two bf16 parts in
  * the kernel for few queries); out is rounded once.
  *

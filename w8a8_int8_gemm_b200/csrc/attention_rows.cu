@@ -374,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int i = (row0 + r) / p.group;
     const int head = kv_head * p.group + (row0 + r) % p.group;
     const int64_t token = doc.q0 + i;
-    // No key left: 0 (and a logarithm of -inf).
-    const bool any = key_limit(p, doc, i) > 0;
+    // No key left, or none with a weight (scores of -inf): 0 (and a logarithm of -inf).
+    const bool any = sum != 0.0f;
     const float inv = any ? 1.0f / sum : 0.0f;
     *reinterpret_cast<uint32_t*>(p.out + token * p.ldo + head * p.hso + col) =
         any ? pack_bf16(x0 * inv, x1 * inv) : 0u;

@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after_sync();
       if (n > 0) l += partner(l);
-      const bool any = limit > 0;
+      const bool any = l != 0.0f;  // (a key that is seen, with a score above -inf)
       const float inv = any ? 1.0f / l : 0.0f;
       const int64_t token = doc.q0 + i;
       // The warp's 32 rows x D/2 values, 32 columns at a time through shared memory, so that they leave in segments
