@@ -4,7 +4,8 @@ The functions below have the names of the C entry points in
 ``include/w8a8.h`` and do argument marshalling only: they check that the
 torch tensors have the layout the C ABI expects, allocate outputs the
 caller did not pass (torch is used for device memory and streams), and call
-the library on the current CUDA stream.  (For the calls whose smallest cases
+the library on the current CUDA stream, or on the ``stream`` of the call, to
+which the tensors that it allocates then belong.  (For the calls whose smallest cases
 are bound by the host that is done natively, in csrc/binding.cpp.)  Every
 step of the computation runs in the library's CUDA kernels; there is no
 fallback.  If the shared objects have not been built, importing this package
@@ -18,6 +19,7 @@ per-channel dequantization plus bias folded into the GEMM epilogue, bf16 out.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -232,6 +234,32 @@ def _need_contig(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -
         raise ValueError(f"{name} must be contiguous")
 
 
+def _on(stream, device: torch.device):
+    """The context of a call's stream (None: the current one), in which it allocates."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (a handle of 0 is the default stream, but to ExternalStream it is none)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(like: torch.Tensor, shape: tuple, dtype: torch.dtype, stream) -> torch.Tensor:
+    """A new tensor beside `like` that belongs to the stream of the call: memory of another stream could be handed
+    out again by that stream before this one's kernels are done with it."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on(stream, like.device):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _zeros(like: torch.Tensor, shape: tuple, dtype: torch.dtype, stream) -> torch.Tensor:
+    """The same, of zeros that the call's kernels find there."""
+    with _on(stream, like.device):
+        return like.new_zeros(shape, dtype=dtype)
+
+
 def _cfg(config) -> GemmConfig | None:
     if config is None:
         return None
@@ -260,9 +288,9 @@ def w8a8_quantize_act(x: torch.Tensor, xq: torch.Tensor | None = None, scale_a: 
     _need(x, "x", torch.bfloat16, 2)
     M, K = x.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        xq = _empty(x, (M, K), torch.int8, stream)
     if scale_a is None:
-        scale_a = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scale_a = _empty(x, (M,), torch.float32, stream)
     _need(xq, "xq", torch.int8, 2)
     if tuple(xq.shape) != (M, K):
         raise ValueError("xq must have the shape of x")
@@ -279,9 +307,9 @@ def w8a8_quantize_weight(w: torch.Tensor, wq: torch.Tensor | None = None, scale_
     _need(w, "w", torch.float32, 2)
     N, K = w.shape
     if wq is None:
-        wq = torch.empty((N, K), dtype=torch.int8, device=w.device)
+        wq = _empty(w, (N, K), torch.int8, stream)
     if scale_w is None:
-        scale_w = torch.empty((N,), dtype=torch.float32, device=w.device)
+        scale_w = _empty(w, (N,), torch.float32, stream)
     _need(wq, "wq", torch.int8, 2)
     if tuple(wq.shape) != (N, K):
         raise ValueError("wq must have the shape of w")
@@ -312,7 +340,7 @@ def w8a8_gemm_ex(xq, wq, scale_a, scale_w, bias=None, out=None, config=None, str
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty(xq, (M, N), torch.bfloat16, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     c = _cfg(config)
     st = _lib.w8a8_gemm_ex(_ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K,
@@ -329,7 +357,7 @@ def w8a8_gemm(xq, wq, scale_a, scale_w, bias=None, out=None, stream=None):
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty(xq, (M, N), torch.bfloat16, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _check(_lib.w8a8_gemm(_ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K,
                           _stream(stream, xq.device)), "w8a8_gemm")
@@ -340,7 +368,7 @@ def w8a8_gemm_i32(xq, wq, acc=None, stream=None, config=None):
     """Raw int32 accumulators acc [M, N] = xq @ wq^T (exact)."""
     M, N, K = _gemm_operands(xq, wq)
     if acc is None:
-        acc = torch.empty((M, N), dtype=torch.int32, device=xq.device)
+        acc = _empty(xq, (M, N), torch.int32, stream)
     _need_contig(acc, "acc", torch.int32, (M, N))
     if config is None:
         st = _lib.w8a8_gemm_i32(_ptr(xq), _ptr(wq), _ptr(acc), M, N, K, _stream(stream, xq.device))
@@ -372,18 +400,17 @@ def w8a8_linear(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=None
     _need_contig(scale_w, "scale_w", torch.float32, (N,))
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
-    dev = x.device
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty(x, (M, N), torch.bfloat16, stream)
     if ws_xq is None:
-        ws_xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        ws_xq = _empty(x, (M, K), torch.int8, stream)
     if ws_scale_a is None:
-        ws_scale_a = torch.empty((M,), dtype=torch.float32, device=dev)
+        ws_scale_a = _empty(x, (M,), torch.float32, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _need_contig(ws_xq, "ws_xq", torch.int8, (M, K))
     _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
     _check(_lib.w8a8_linear(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq),
-                            _ptr(ws_scale_a), M, N, K, _stream(stream, dev)), "w8a8_linear")
+                            _ptr(ws_scale_a), M, N, K, _stream(stream, x.device)), "w8a8_linear")
     return out
 
 
@@ -409,21 +436,20 @@ def w8a8_linear_fused(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_
     _need_contig(scale_w, "scale_w", torch.float32, (N,))
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
-    dev = x.device
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty(x, (M, N), torch.bfloat16, stream)
     if ws_xq is None:
-        ws_xq = torch.empty((M, K), dtype=torch.int8, device=dev)
+        ws_xq = _empty(x, (M, K), torch.int8, stream)
     if ws_scale_a is None:
-        ws_scale_a = torch.empty((M,), dtype=torch.float32, device=dev)
+        ws_scale_a = _empty(x, (M,), torch.float32, stream)
     if ws_sync is None:
-        ws_sync = torch.zeros((w8a8_linear_sync_words(M),), dtype=torch.int32, device=dev)
+        ws_sync = _zeros(x, (w8a8_linear_sync_words(M),), torch.int32, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _need_contig(ws_xq, "ws_xq", torch.int8, (M, K))
     _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
     _need_contig(ws_sync, "ws_sync", torch.int32, (w8a8_linear_sync_words(M),))
     _check(_lib.w8a8_linear_fused(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq),
-                                  _ptr(ws_scale_a), _ptr(ws_sync), M, N, K, _stream(stream, dev)),
+                                  _ptr(ws_scale_a), _ptr(ws_sync), M, N, K, _stream(stream, x.device)),
            "w8a8_linear_fused")
     return out
 
@@ -446,7 +472,7 @@ def w8a8_linear_noalloc(x, wq, scale_w, bias=None, out=None, stream=None):
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        out = _empty(x, (M, N), torch.bfloat16, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _check(_lib.w8a8_linear_noalloc(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K,
                                     _stream(stream, x.device)), "w8a8_linear_noalloc")
@@ -462,9 +488,9 @@ def _quantize_fp8(fn, what, src, dtype, q, scale, stream):
     _need(src, "x" if dtype == torch.bfloat16 else "w", dtype, 2)
     R, K = src.shape
     if q is None:
-        q = torch.empty((R, K), dtype=torch.uint8, device=src.device)
+        q = _empty(src, (R, K), torch.uint8, stream)
     if scale is None:
-        scale = torch.empty((R,), dtype=torch.float32, device=src.device)
+        scale = _empty(src, (R,), torch.float32, stream)
     _need(q, "codes", torch.uint8, 2)
     if tuple(q.shape) != (R, K):
         raise ValueError("the codes must have the shape of the input")
@@ -506,7 +532,7 @@ def w8a8_gemm_fp8_ex(xq, wq, scale_a, scale_w, bias=None, out=None, config=None,
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty(xq, (M, N), torch.bfloat16, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     c = _cfg(config)
     st = _lib.w8a8_gemm_fp8_ex(_ptr(xq), _ptr(wq), _ptr(scale_a), _ptr(scale_w), _ptr(bias), _ptr(out), M, N, K,
@@ -524,7 +550,7 @@ def w8a8_gemm_fp8_f32(xq, wq, acc=None, stream=None, config=None):
     """Raw fp32 accumulators acc [M, N] of the E4M3 product xq @ wq^T."""
     M, N, K = _fp8_operands(xq, wq)
     if acc is None:
-        acc = torch.empty((M, N), dtype=torch.float32, device=xq.device)
+        acc = _empty(xq, (M, N), torch.float32, stream)
     _need_contig(acc, "acc", torch.float32, (M, N))
     c = _cfg(config)
     st = _lib.w8a8_gemm_fp8_f32_ex(_ptr(xq), _ptr(wq), _ptr(acc), M, N, K,
@@ -550,18 +576,17 @@ def w8a8_linear_fp8(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=
     _need_contig(scale_w, "scale_w", torch.float32, (N,))
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
-    dev = x.device
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        out = _empty(x, (M, N), torch.bfloat16, stream)
     if ws_xq is None:
-        ws_xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        ws_xq = _empty(x, (M, K), torch.uint8, stream)
     if ws_scale_a is None:
-        ws_scale_a = torch.empty((M,), dtype=torch.float32, device=dev)
+        ws_scale_a = _empty(x, (M,), torch.float32, stream)
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _need_contig(ws_xq, "ws_xq", torch.uint8, (M, K))
     _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
     _check(_lib.w8a8_linear_fp8(_ptr(x), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(out), _ptr(ws_xq),
-                                _ptr(ws_scale_a), M, N, K, _stream(stream, dev)), "w8a8_linear_fp8")
+                                _ptr(ws_scale_a), M, N, K, _stream(stream, x.device)), "w8a8_linear_fp8")
     return out
 
 
@@ -573,9 +598,9 @@ def w8a8_quantize_act_gelu(h, xq=None, scale_a=None, stream=None):
     _need(h, "h", torch.bfloat16, 2)
     M, K = h.shape
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.int8, device=h.device)
+        xq = _empty(h, (M, K), torch.int8, stream)
     if scale_a is None:
-        scale_a = torch.empty((M,), dtype=torch.float32, device=h.device)
+        scale_a = _empty(h, (M,), torch.float32, stream)
     _need(xq, "xq", torch.int8, 2)
     if tuple(xq.shape) != (M, K):
         raise ValueError("xq must have the shape of h")
@@ -590,7 +615,7 @@ def w8a8_gelu(h, g=None, stream=None):
     _need(h, "h", torch.bfloat16, 2)
     M, K = h.shape
     if g is None:
-        g = torch.empty((M, K), dtype=torch.bfloat16, device=h.device)
+        g = _empty(h, (M, K), torch.bfloat16, stream)
     _need(g, "g", torch.bfloat16, 2)
     if tuple(g.shape) != (M, K):
         raise ValueError("g must have the shape of h")
@@ -601,7 +626,7 @@ def w8a8_gelu(h, g=None, stream=None):
 
 def w8a8_linear_gelu(h, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=None, stream=None):
     """out bf16 [M, N] = GELU(h) W^T + b: w8a8_quantize_act_gelu then w8a8_gemm."""
-    l = linear_layer(h, wq, scale_w, bias, out, ws_xq, ws_scale_a, ACT_GELU)
+    l = linear_layer(h, wq, scale_w, bias, out, ws_xq, ws_scale_a, ACT_GELU, stream=stream)
     _check(_lib.w8a8_linear_gelu(_ptr(l["x"]), _ptr(wq), _ptr(scale_w), _ptr(bias), _ptr(l["out"]),
                                  _ptr(l["ws_xq"]), _ptr(l["ws_scale_a"]), l["M"], l["N"], l["K"],
                                  _stream(stream, h.device)), "w8a8_linear_gelu")
@@ -609,17 +634,6 @@ def w8a8_linear_gelu(h, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a
 
 
 # ------------------------------------------------- the gated linear layer
-
-
-def _empty(like: torch.Tensor, shape: tuple, dtype: torch.dtype, stream) -> torch.Tensor:
-    """A new tensor beside `like` that belongs to the stream of the call: memory of another stream could be handed
-    out again by that stream before this one's kernels are done with it."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
 
 
 def _gemm_glu(fn, what, code, xq, wq, scale_a, scale_w, bias, out, act, config, stream):
@@ -752,9 +766,9 @@ def w8a8_attention(q, k, v, scale: float | None = None, cap: float = 0.0, causal
 
 
 def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=None, input_act: int = ACT_NONE,
-                 output_glu: int = ACT_NONE) -> dict:
+                 output_glu: int = ACT_NONE, stream=None) -> dict:
     """One layer of a chain: the tensors of a w8a8_linear call, with the
-    output and workspace allocated here when not given.  x may be an
+    output and workspace allocated here (on ``stream``) when not given.  x may be an
     earlier layer's ``out``; input_act=ACT_GELU makes the layer compute
     GELU(x) W^T + b (w8a8_linear_gelu); output_glu=ACT_SILU or ACT_GELU
     makes it a gated one (w8a8_linear_glu), with wq [2N, K]."""
@@ -763,7 +777,8 @@ def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=Non
     if output_glu != ACT_NONE:
         _need_contig(x, "x", torch.bfloat16, (M, K))
         N = _glu_weight(wq, torch.int8, K, scale_w, bias)
-        return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu)
+        return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu,
+                              stream)
     _need(wq, "wq", torch.int8, 2)
     N = wq.shape[0]
     if wq.shape[1] != K:
@@ -773,14 +788,13 @@ def linear_layer(x, wq, scale_w, bias=None, out=None, ws_xq=None, ws_scale_a=Non
     _need_contig(scale_w, "scale_w", torch.float32, (N,))
     if bias is not None:
         _need_contig(bias, "bias", torch.bfloat16, (N,))
-    return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, ACT_NONE)
+    return _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, ACT_NONE, stream)
 
 
-def _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu) -> dict:
-    dev = x.device
-    out = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if out is None else out
-    ws_xq = torch.empty((M, K), dtype=torch.int8, device=dev) if ws_xq is None else ws_xq
-    ws_scale_a = torch.empty((M,), dtype=torch.float32, device=dev) if ws_scale_a is None else ws_scale_a
+def _layer_buffers(x, wq, scale_w, bias, out, ws_xq, ws_scale_a, M, N, K, input_act, output_glu, stream) -> dict:
+    out = _empty(x, (M, N), torch.bfloat16, stream) if out is None else out
+    ws_xq = _empty(x, (M, K), torch.int8, stream) if ws_xq is None else ws_xq
+    ws_scale_a = _empty(x, (M,), torch.float32, stream) if ws_scale_a is None else ws_scale_a
     _need_contig(out, "out", torch.bfloat16, (M, N))
     _need_contig(ws_xq, "ws_xq", torch.int8, (M, K))
     _need_contig(ws_scale_a, "ws_scale_a", torch.float32, (M,))
