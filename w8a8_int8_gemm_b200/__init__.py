@@ -165,7 +165,9 @@ def _load_calls():
         from . import _calls as calls
     except ImportError as e:
         raise ImportError(f"_calls.so is missing or does not load ({e}): {again}") from e
-    if calls.torch_version != torch.__version__.split("+")[0]:
+    # (its version is the release's three numbers; a nightly's or a vendor's torch adds a label to them)
+    release = re.match(r"\d+\.\d+\.\d+", torch.__version__)
+    if release is None or calls.torch_version != release[0]:
         raise ImportError(f"_calls.so was built against torch {calls.torch_version}, not {torch.__version__}: {again}")
     return calls
 
