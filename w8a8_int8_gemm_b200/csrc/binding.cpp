@@ -101,6 +101,13 @@ T* optional(PyObject* o, const char* name, ScalarType type, at::IntArrayRef shap
   return o == Py_None ? nullptr : static_cast<T*>(contiguous(o, name, type, shape, dev).data_ptr());
 }
 
+// A table's data.  One without entries has no address of its own, and null would say that there is no table: it gets
+// one that is never read.
+const float* table(PyObject* o, const char* name, at::IntArrayRef shape, Device& dev) {
+  const float* data = optional<const float>(o, name, ScalarType::Float, shape, dev);
+  return data != nullptr ? data : reinterpret_cast<const float*>(uintptr_t{16});
+}
+
 // A bf16 [tokens, heads, head_dim] view: its sizes and strides in elements.
 struct Heads {
   void* data;
@@ -223,8 +230,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(cos, "cos", ScalarType::Float, 2);
       d.table_rows = cos.size(0);
       d.rot_dim = narrow(2 * cos.size(1));
-      d.cos = optional<const float>(a[4], "cos", ScalarType::Float, cos.sizes(), dev);
-      d.sin = optional<const float>(a[5], "sin", ScalarType::Float, cos.sizes(), dev);
+      d.cos = table(a[4], "cos", cos.sizes(), dev);
+      d.sin = table(a[5], "sin", cos.sizes(), dev);
     }
     d.positions = optional<const int32_t>(a[6], "positions", ScalarType::Int, {hq.rows}, dev);
     d.eps = static_cast<float>(number(a[7]));
