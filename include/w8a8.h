@@ -384,8 +384,8 @@ W8A8_API w8a8_status w8a8_linear_glu_fp8(const void* x, const uint8_t* wq, const
  *
  *   q, k        bf16 [M, heads, head_dim], the last dimension contiguous, ld*
  *               the stride of a token and hs* of a head, in elements (multiples
- *               of 8, 0 allowed for inputs): views into one QKV buffer, or
- *               head-major tensors.  heads_q or heads_k may be 0 (its pointers
+ *               of 8 below 2^31, 0 allowed for inputs): views into one QKV
+ *               buffer, or head-major tensors.  heads_q or heads_k may be 0 (its pointers
  *               are then not used).
  *   q_out,k_out the same shapes with their own strides; the heads of an output
  *               may not overlap one another.  An output may be its own input
@@ -444,9 +444,9 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  *
  *   q, out   bf16 [tokens_q, heads_q, head_dim];  k, v  bf16 [tokens_k, heads_k,
  *            head_dim]: the last dimension contiguous, ld* the stride of a
- *            token and hs* of a head in elements (multiples of 8, at least
- *            head_dim where there is more than one): views of a QKV buffer or
- *            head-major tensors.  out's rows may not overlap one another, nor
+ *            token and hs* of a head in elements (multiples of 8 below 2^31, at
+ *            least head_dim where there is more than one): views of a QKV
+ *            buffer or head-major tensors.  out's rows may not overlap one another, nor
  *            any other argument.
  *   lse      fp32 [tokens_q, heads_q] contiguous, or NULL
  *   cu_q, cu_k  int32 [docs + 1] on the device, not decreasing: document d has

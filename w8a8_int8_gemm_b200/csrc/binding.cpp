@@ -19,7 +19,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
-#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -116,8 +115,9 @@ struct Heads {
 
 Heads view(const Tensor& t) {
   Heads h{t.data_ptr(), t.size(0), t.size(1), t.size(2), t.stride(0), t.stride(1)};
-  if (h.heads <= 1) h.hs = h.dim;  // (the stride of a dimension of one is free)
-  if (h.rows <= 1) h.ld = std::max<int64_t>(1, h.heads) * h.hs;
+  // (the stride of a dimension of one is free)
+  if (h.heads <= 1) h.hs = h.dim;
+  if (h.rows <= 1) h.ld = h.dim;
   return h;
 }
 
