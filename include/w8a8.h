@@ -454,7 +454,9 @@ W8A8_API w8a8_status w8a8_qk_norm_rope(const w8a8_qk_desc* desc, w8a8_stream_t s
  *            of tokens is then a multiple of docs).  Documents may be empty;
  *            tokens before cu[0] and from cu[docs] on belong to none, and their
  *            rows of out and lse are left as they were.  Values are clamped to
- *            [0, tokens]; decreasing ones give unspecified rows of out.
+ *            [0, tokens]; decreasing ones give unspecified rows of out.  (Caches
+ *            that lie apart in one buffer, each with room to grow, are documents
+ *            with documents of no queries, the unused room, between them.)
  *   prefix   int32 [docs] on the device or NULL; only with causal
  *   slopes   fp32 [heads_q] on the device or NULL
  * Keys, values and queries outside a document, whatever they hold, do not
