@@ -91,7 +91,13 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // when that leaves at least half the units idle; a tile costs its
 // multiply-adds times its relative cost, plus a fixed fill / drain overhead
 // of two K blocks.
-w8a8_gemm_config select(int64_t M, int64_t N, int64_t K, int sms, bool allow_pair = true) {
+// The gated layer (N: the columns of both projections) makes no half-width
+// items on single CTAs.  Where K % 128 != 0 the whole round is charged: on 21
+// shapes that then go to pairs 0.93 of the time on average, 0.69 to 1.11 (1463
+// tokens, N 4864, K 1936: 43.1 -> 32.4 us).  Where K % 128 == 0 the pair's 0.88
+// is too low for this epilogue by more than the half round: charged, 13 shapes
+// took 1.11 of the time on average, so it is not.
+w8a8_gemm_config select(int64_t M, int64_t N, int64_t K, int sms, bool allow_pair = true, bool gated = false) {
   struct Cand { int bm, bn; double rel_cost; int raster; };
   const double pair_cost = K % 128 == 0 ? 0.88 : 1.02;
   const Cand cands[4] = {{128, 256, 1.00, 1}, {256, 256, pair_cost, 1}, {128, 128, 1.75, 1}, {256, 128, 1.90, 8}};
@@ -105,7 +111,8 @@ w8a8_gemm_config select(int64_t M, int64_t N, int64_t K, int sms, bool allow_pai
     // rounds of tiles per unit; a short last round of 256-column tiles runs
     // as half-width items (half a round)
     const int64_t tail = tiles % units;
-    const double per_unit = (c.bn == 256 && tail > 0 && 2 * tail <= units && tiles > units)
+    const bool halves = c.bn == 256 && !(gated && c.bm == 128 && K % 128 != 0);
+    const double per_unit = (halves && tail > 0 && 2 * tail <= units && tiles > units)
                                 ? static_cast<double>(tiles / units) + 0.5
                                 : static_cast<double>(ceil_div(tiles, units));
     const double macs_per_sm = static_cast<double>(c.bm / (c.bm == 256 ? 2 : 1)) * c.bn;
@@ -141,7 +148,8 @@ w8a8_status gemm_common(const int8_t* xq, const int8_t* wq, const float* scale_a
   DeviceInfo dev;
   if ((st = current_device(&dev)) != W8A8_OK) return st;
   // (the gated layer's product has the columns of both projections)
-  const w8a8_gemm_config cfg = user_cfg ? *user_cfg : select(M, kind == GemmOut::kGlu ? 2 * N : N, K, dev.sms);
+  const bool gated = kind == GemmOut::kGlu;
+  const w8a8_gemm_config cfg = user_cfg ? *user_cfg : select(M, gated ? 2 * N : N, K, dev.sms, true, gated);
   GemmArgs a;
   a.act = act;
   a.xq = xq;

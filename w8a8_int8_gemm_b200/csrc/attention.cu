@@ -11,8 +11,6 @@ using namespace w8a8;
 
 namespace {
 
-constexpr int64_t kMaxStride = 2147483640;  // elements; keeps token * stride within 63 bits
-
 struct View {
   const void* ptr;
   int64_t tokens, ld, heads, hs;

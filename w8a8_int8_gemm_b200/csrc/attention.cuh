@@ -144,6 +144,11 @@ __device__ __forceinline__ int key_limit(const AttnParams& p, const Doc& d, int 
   return p.causal ? min(max(i + d.shift + 1, d.prefix), d.lk) : d.lk;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -63,11 +63,6 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t addr) {  
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 __device__ __forceinline__ float low_part(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_part(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

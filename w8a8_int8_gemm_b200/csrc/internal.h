@@ -132,6 +132,7 @@ cudaError_t allow_shared_memory(Kernel kernel, int bytes, std::atomic<uint64_t>&
   if (e == cudaSuccess) mask.fetch_or(bit, std::memory_order_release);
   return e;
 }
+constexpr int64_t kMaxStride = 2147483640;  // elements; keeps token * stride within 63 bits
 bool rows_disjoint(int64_t rows, int64_t ld, int64_t heads, int64_t hs, int64_t dim);
 
 // Synchronizes the current device and reads (optionally clears) the device

@@ -194,8 +194,6 @@ cudaError_t launch(const QkParams& p, bool pairs, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-constexpr int64_t kMaxStride = 2147483640;  // elements; keeps m * stride within 63 bits
-
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 
 }  // namespace
