@@ -149,6 +149,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tail_rows;         // rows of the last V tile that are the document's
     bool tail;             // ... and not all of them
   };
+  // A warp that has nothing to do in an item, or waits for its end, waits as long as the item takes, some 1 us a tile:
+  // its limit grows with the tiles.  (If the others stop, they find out within their own limits and raise the flag.)
+  int item_tiles = 0;
+  const auto item_limit = [&] { return p.timeout_ns + 100000ull * static_cast<uint64_t>(item_tiles); };
   const auto item_of = [&](int x) {
     Item it;
     it.head = p.causal ? x % p.heads_q : x / slots;
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     it.n0 = key_tiles(0);
     it.n1 = key_tiles(1);
-    it.tiles = max(it.n0, it.n1);
+    it.tiles = item_tiles = max(it.n0, it.n1);
     it.tail_rows = it.doc.lk - (it.tiles - 1) * kTileK;
     it.tail = it.tiles > 0 && it.tail_rows < kTileK;
     return it;
@@ -174,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++taken;
     const int b = taken & 1;
     const bool got = mbar_wait_bounded(&item_full[b], static_cast<uint32_t>((taken - 1) >> 1) & 1u, abort_flag,
-                                       p.timeout_ns, err, kSiteAttnItem);
+                                       item_limit(), err, kSiteAttnItem);
     if (!__all_sync(0xFFFFFFFFu, got)) return -1;
     const int x = launch_cancelled(answer + 16 * b);
     __syncwarp();
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item it = item_of(item);
         fills = (fills + 2 * it.tiles) % kStages;  // the ring slot behind the item's last V tile
         if (!it.tail) continue;
-        ok = warp_wait(&tail_full[tails & 1], static_cast<uint32_t>(tails >> 1) & 1u, abort_flag, p.timeout_ns, err,
+        ok = warp_wait(&tail_full[tails & 1], static_cast<uint32_t>(tails >> 1) & 1u, abort_flag, item_limit(), err,
                        kSiteAttnOperand);
         if (!ok) continue;
         const int stage = (fills + kStages - 1) % kStages;
