@@ -17,7 +17,7 @@
 // starts or joins: 190 KB in flight per SM.  (Loads straight to the fragments'
 // registers, one step ahead, kept 64 KB in flight with one CTA per SM, which
 // left 16 sequences with 192 000 cached tokens, 32 heads over 8 of 128, at 237
-// us; now 131 us, 6.0 TB/s, 0.92 of the measured copy rate.)
+// us; now 128-131 us, 6.0 TB/s, 0.92 of the measured copy rate.)
 //
 // P is split into two bf16 parts (p = hi + lo, 16 bits in all): the second
 // product is free here, and the output then carries one bf16 rounding, its

@@ -44,7 +44,7 @@
 // Measured, in graphs of calls: 2 x 4608 tokens, 24 heads of 128: 412 us, 1.27
 // PFLOP/s, 0.76 of the measured bf16 rate (484 us in a loop of seconds, where
 // the board's power cap sets the clock); 2 x 4095 tokens, 16 heads of 128,
-// causal, with slopes: 161 us; 9 ragged prompts of 911 tokens on average, cap
+// causal, with slopes: 162 us; 9 ragged prompts of 911 tokens on average, cap
 // and prefix, 16 heads of 64 over 4: 68 us.
 #include <cuda.h>
 
